@@ -93,8 +93,15 @@ typedef enum {
   KVQ_ERR_BAD_SIZE = 7,       /* negative or too large count / position     */
   KVQ_ERR_DEVICE_TIMEOUT = 8, /* a kernel gave up waiting for its own copy  */
   KVQ_ERR_UNSUPPORTED_DEVICE = 9, /* device is not compute capability 10.0 */
-  KVQ_ERR_BAD_BITS = 10       /* code width not 3 (d >= 128), 4, 6 or 8     */
+  KVQ_ERR_BAD_BITS = 10,      /* code width not 3 (d >= 128), 4, 6 or 8     */
+  KVQ_ERR_BAD_INDEX = 11,     /* a kernel met a position, slot, page or
+                                 length outside its range and skipped it   */
+  KVQ_ERR_BAD_DTYPE = 12      /* dtype is neither KVQ_F16 nor KVQ_BF16      */
 } kvq_status;
+
+/* Element type of activations (queries, new keys and values, outputs) in the
+ * calls that take a `dtype`; the calls without one take fp16. */
+typedef enum { KVQ_F16 = 0, KVQ_BF16 = 1 } kvq_dtype;
 
 /*
  * Forward step ("First, the 17%"; "Fusing four steps into two kernels is not
@@ -280,15 +287,156 @@ KVQ_API kvq_status kvq_attend_decode(const uint16_t *q, const uint8_t *k_packed,
                                      int32_t group, const int8_t *signs, kvq_rot rot,
                                      float sm_scale, uint16_t *out, kvq_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Paged cache: position rotation, append, attention of new tokens.
+ *
+ * The int4 cache of one layer in pages of page_size tokens, so that sequences
+ * of any length share one pool.  A page row is a row of kvq_rot_quant_fwd
+ * (same codes, nibble order, scales, D and R), so kvq_dequant_rot_inv reads a
+ * pool back.  Activations are fp16 or bf16; rows of a token may lie inside a
+ * wider buffer (a fused projection), which the token strides say (in
+ * elements, a multiple of 8, at least heads * d).
+ *
+ * Values on the device that are out of range (a position, slot, page number
+ * or length) are never followed: the row concerned is skipped as each call
+ * states, and kvq_device_status returns KVQ_ERR_BAD_INDEX.
+ * ------------------------------------------------------------------------ */
+
+/* Page pool of one layer. */
+typedef struct {
+  uint8_t *k_packed, *v_packed; /* [n_pages][n_kv_heads][page_size][d/2], 16-byte aligned */
+  float *k_scales, *v_scales;   /* [n_pages][n_kv_heads][page_size][d/g], 16-byte aligned */
+  int64_t n_pages;              /* 1 .. 2^31 - 1                                  */
+  int32_t n_kv_heads;           /* 1 .. 65535                                     */
+  int32_t page_size;            /* 16, 32, 64, 128 or 256 tokens                  */
+  int32_t d, group;             /* as in kvq_rot_quant_fwd                        */
+  const int8_t *signs;          /* [d], as in kvq_rot_quant_fwd                   */
+  kvq_rot rot;
+} kvq_paged_cache;
+
+/* Norm of a head's row and rotation by its position, in fp32:
+ *   n = x * rsqrt(mean(x^2) + eps) * weight         (weight not NULL)
+ *   the first rot_dim values in pairs (a, b) = (n[i], n[i + rot_dim/2]), or
+ *   (n[2i], n[2i+1]) if interleaved, i < rot_dim/2, become
+ *   (a cos - b sin, a sin + b cos) with row `position` of the table; the
+ *   values from rot_dim on pass through            (cos_sin not NULL). */
+typedef struct {
+  const float *cos_sin; /* [n_pos][rot_dim]: rot_dim/2 cosines, then as many sines;
+                           16-byte aligned; NULL: no rotation                 */
+  int64_t n_pos;        /* 1 .. 2^31 - 1                                      */
+  int32_t rot_dim;      /* a multiple of 16, 16 .. d                          */
+  int32_t interleaved;  /* non-zero: neighbours are pairs                     */
+  float eps;            /* of the norm; finite, >= 0                          */
+} kvq_rope;
+
+/*
+ * Norm and position rotation of the queries, and of the keys, of n_tokens
+ * tokens in one pass.
+ *
+ *   q          [n_tokens][n_heads][d], token stride q_stride (read)
+ *   k          [n_tokens][n_k_heads][d], token stride k_stride (read);
+ *              NULL with n_k_heads == 0: queries only
+ *   positions  [n_tokens] int32 (NULL without a rotation).  A token at a
+ *              negative position is padding: its rows are left as they were.
+ *              So are those of a position >= n_pos (KVQ_ERR_BAD_INDEX).
+ *   q_weight, k_weight  [d] fp32, 16-byte aligned, or NULL: no norm
+ *   q_out, k_out  as q and k, token strides q_out_stride, k_out_stride
+ *              (written); rounded once, to dtype.  They may be q and k
+ *              themselves (same pointer and stride); they must not overlap
+ *              the inputs in any other way.
+ *   n_tokens 0..2^31-1 (0: no-op), n_heads 1..65535, n_k_heads 0..65535;
+ *   d 64 / 128 / 256; data 16-byte aligned.
+ */
+KVQ_API kvq_status kvq_qk_norm_rope(const void *q, const void *k, kvq_dtype dtype,
+                                    int64_t n_tokens, int32_t n_heads, int32_t n_k_heads,
+                                    int32_t d, int64_t q_stride, int64_t k_stride,
+                                    const int32_t *positions, const float *q_weight,
+                                    const float *k_weight, const kvq_rope *rope, void *q_out,
+                                    void *k_out, int64_t q_out_stride, int64_t k_out_stride,
+                                    kvq_stream stream);
+
+/*
+ * Append: the keys and values of n_tokens new tokens become rows of the page
+ * pool.  k goes through norm and rotation (rope, k_weight; either may be
+ * absent), then k and v through the forward step; nothing is rounded in
+ * between.
+ *
+ *   k, v       [n_tokens][n_kv_heads][d], token strides k_stride, v_stride (read)
+ *   slots      [n_tokens] int64: page * page_size + row in the page.  A
+ *              negative slot is padding: the token is skipped, and so is one
+ *              with a slot past the pool or a position outside the table
+ *              (KVQ_ERR_BAD_INDEX).  The slots of a call must differ: two
+ *              tokens with one slot leave a row with parts of both.
+ *   positions  [n_tokens] int32 (NULL without a rotation)
+ *   k_weight   [d] fp32, 16-byte aligned, or NULL: no norm
+ *   rope       NULL: neither norm nor rotation
+ *   k_hat, v_hat  [n_tokens][n_kv_heads][d] of dtype, contiguous, 16-byte
+ *              aligned (written), or NULL: the values the new rows stand for,
+ *              i.e. the inverse step of the fresh codes.  Rows of skipped
+ *              tokens are left as they were.
+ *   n_tokens 0..2^31-1 (0: no-op); other arguments as above.
+ */
+KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtype,
+                                    int64_t n_tokens, int64_t k_stride, int64_t v_stride,
+                                    const int64_t *slots, const int32_t *positions,
+                                    const float *k_weight, const kvq_rope *rope,
+                                    const kvq_paged_cache *cache, void *k_hat, void *v_hat,
+                                    kvq_stream stream);
+
+/*
+ * Attention of new tokens (a decoded token, a few drafted ones, a chunk of a
+ * prompt) over the paged cache, which already holds their keys and values.
+ *
+ * Sequence s owns the tokens cu_q[s] .. cu_q[s+1]-1 of q and the first
+ * kv_len[s] cached rows of its pages: row t is row t % page_size of page
+ * page_table[s][t / page_size].  Its i-th of n new tokens stands at position
+ * p = kv_len[s] - n + i and attends the rows t with t <= p and, with a
+ * window, t > p - window.  With K_t, V_t as in kvq_attend_decode, query head
+ * h of that token and KV head h / n_q:
+ *   s_t = sm_scale <q, K_t>,  out = sum_t softmax(s)_t V_t, rounded to dtype.
+ * A token that attends no row gets zeros.  Rows of out that belong to no
+ * sequence are left as they were.
+ *
+ *   q          [n_tokens][n_kv_heads * n_q][d], token stride q_stride (read)
+ *   out        same, token stride out_stride (written); must not overlap q
+ *   cu_q       [n_seqs + 1] int32, non-decreasing, 0 .. n_tokens
+ *   kv_len     [n_seqs] int32, 0 .. max_pages * page_size
+ *   page_table [n_seqs][max_pages] int32; entries past a sequence's last
+ *              page are not read.  Rows of a page outside the pool are not
+ *              attended, and a sequence whose cu_q or kv_len is out of range
+ *              is treated as having no tokens (KVQ_ERR_BAD_INDEX).
+ *   n_q        1..64 queries per KV head; n_kv_heads * n_q <= 65535
+ *   max_q_len  the largest number of new tokens of a sequence: a hint that
+ *              chooses the kernel; the result is right for any value >= 1
+ *   window     0: none
+ *   workspace  kvq_paged_attend_workspace() bytes of device memory, 256-byte
+ *              aligned, used by this call alone until it has finished
+ *   n_tokens 0..2^31-1, n_seqs 0..65535 (0: no-op)
+ */
+KVQ_API kvq_status kvq_paged_attend(const void *q, kvq_dtype dtype, int64_t n_tokens,
+                                    int64_t q_stride, const kvq_paged_cache *cache,
+                                    const int32_t *cu_q, const int32_t *kv_len,
+                                    const int32_t *page_table, int64_t n_seqs,
+                                    int64_t max_pages, int32_t n_q, int32_t max_q_len,
+                                    int32_t window, float sm_scale, void *out,
+                                    int64_t out_stride, void *workspace,
+                                    int64_t workspace_bytes, kvq_stream stream);
+
+/* Bytes of workspace of kvq_paged_attend on the current device for these
+ * sizes (as passed to it); negative: minus a kvq_status. */
+KVQ_API int64_t kvq_paged_attend_workspace(int64_t n_tokens, int32_t n_kv_heads, int32_t n_q,
+                                           int32_t d, int32_t max_q_len);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 KVQ_API const char *kvq_status_string(kvq_status s);
 
 /*
  * Device-side error word of the current device.  The kernels bound every
  * wait on their own asynchronous copies; a wait that runs out records
- * KVQ_ERR_DEVICE_TIMEOUT here and the kernel returns early.  This call
- * synchronizes the device, returns KVQ_OK or the recorded status, and clears
- * the word when `clear` is non-zero.
+ * KVQ_ERR_DEVICE_TIMEOUT here and the kernel returns early.  The paged-cache
+ * kernels record KVQ_ERR_BAD_INDEX for indices out of range.  This call
+ * synchronizes the device, returns KVQ_OK or the recorded status (a time-out
+ * before a bad index), and clears the word when `clear` is non-zero.
  */
 KVQ_API kvq_status kvq_device_status(int32_t clear);
 

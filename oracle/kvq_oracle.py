@@ -74,6 +74,7 @@ __all__ = [
     "pack_nibbles", "unpack_nibbles", "rot_quant_fwd", "dequant_rot_inv",
     "rotated_values", "near_tie_distance", "decode_step", "decode_step_windowed",
     "dequant_rotated_f64", "attend_decode", "pack_codes", "unpack_codes",
+    "norm_rope", "attend_paged",
 ]
 
 
@@ -388,3 +389,67 @@ def attend_decode(q, k_packed, k_scales, v_packed, v_scales, length: int, signs,
         p /= p.sum(axis=1, keepdims=True)
         out[hh] = p @ v
     return out.astype(np.float16)
+
+
+def norm_rope(x, weight, positions, cos_sin, interleaved: bool = False, eps: float = 1e-6):
+    """Norm of each head's row and rotation by its token's position, float64.
+
+    x: [T, H, d]; weight [d] or None (no norm): n = x / sqrt(mean x^2 + eps) * weight.
+    cos_sin: [n_pos, r] (r/2 cosines, then sines) or None (no rotation): the
+    pairs (n[i], n[i + r/2]), or (n[2i], n[2i+1]) when interleaved, are turned
+    by row positions[t]; values from r on pass through.
+    """
+    n = np.asarray(x, dtype=np.float64).copy()
+    if weight is not None:
+        n /= np.sqrt((n * n).mean(axis=-1, keepdims=True) + eps)
+        n *= np.asarray(weight, dtype=np.float64)
+    if cos_sin is None:
+        return n
+    r = cos_sin.shape[1]
+    a_at = np.arange(0, r, 2) if interleaved else np.arange(r // 2)
+    b_at = a_at + (1 if interleaved else r // 2)
+    for t, p in enumerate(positions):
+        c = np.asarray(cos_sin[p, : r // 2], dtype=np.float64)
+        s = np.asarray(cos_sin[p, r // 2:], dtype=np.float64)
+        a, b = n[t][:, a_at].copy(), n[t][:, b_at].copy()
+        n[t][:, a_at] = a * c - b * s
+        n[t][:, b_at] = a * s + b * c
+    return n
+
+
+def attend_paged(q, k_packed, k_scales, v_packed, v_scales, cu_q, kv_len, page_table, signs,
+                 rot: int, group: int, sm_scale: float, window: int = 0):
+    """Causal attention of new tokens over a paged int4 cache, float64.
+
+    Pools [pages, H, page, d/2] uint8 and [pages, H, page, d/g] float32; the
+    i-th of a sequence's n new tokens stands at p = kv_len - n + i and attends
+    the rows t <= p with t > p - window (window 0: all), except rows on pages
+    outside the pool; a token that attends none gets zeros.
+    q: [T, H n_q, d] (any float type); returns [T, H n_q, d] float64, NaN in
+    rows of no sequence.
+    """
+    q = np.asarray(q, dtype=np.float64)
+    t_all, h, d = q.shape
+    pages, hkv, page, _ = k_packed.shape
+    n_q = h // hkv
+    out = np.full(q.shape, np.nan)
+    for s in range(len(kv_len)):
+        a, b, length = int(cu_q[s]), int(cu_q[s + 1]), int(kv_len[s])
+        t = np.arange(length)
+        at = np.asarray(page_table[s])[t // page].astype(np.int64)
+        good = (at >= 0) & (at < pages)
+        at, off = np.where(good, at, 0), t % page
+        for g in range(hkv):
+            k = dequant_rotated_f64(k_packed[at, g, off], k_scales[at, g, off], signs, rot, group)
+            v = dequant_rotated_f64(v_packed[at, g, off], v_scales[at, g, off], signs, rot, group)
+            for i in range(a, b):
+                p = length - (b - a) + (i - a)
+                see = good & (t <= p) & ((t > p - window) if window else True)
+                heads = slice(g * n_q, (g + 1) * n_q)
+                if not see.any():
+                    out[i, heads] = 0.0
+                    continue
+                w = sm_scale * (q[i, heads] @ k[see].T)
+                w = np.exp(w - w.max(axis=1, keepdims=True))
+                out[i, heads] = (w / w.sum(axis=1, keepdims=True)) @ v[see]
+    return out

@@ -23,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvq.so")
 
-SOURCES = ["kvq_api.cu", "kvq_d64.cu", "kvq_d128.cu", "kvq_d256.cu"]
+SOURCES = ["kvq_api.cu", "kvq_d64.cu", "kvq_d128.cu", "kvq_d256.cu", "kvq_paged_api.cu",
+           "kvq_paged_d64.cu", "kvq_paged_d128.cu", "kvq_paged_d256.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # Hidden visibility: only the C API (KVQ_API in include/kvq.h) is exported.
 # Otherwise the function-local statics of inline and template code are

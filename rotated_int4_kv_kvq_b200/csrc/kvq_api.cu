@@ -9,56 +9,14 @@
 #include <mutex>
 
 #include "kvq.h"
+#include "kvq_host.h"
 #include "kvq_launch.h"
+#include "kvq_paged_launch.h"
 
 namespace {
 
+using namespace kvq::host;
 using kvq::vpw_of;
-
-constexpr int kMaxDevices = 64;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-kvq_status check_shape(int32_t d, int32_t group, kvq_rot rot) {
-  if (rot != KVQ_ROT_SRFT && rot != KVQ_ROT_SRHT) return KVQ_ERR_BAD_ROT;
-  if (d != 64 && d != 128 && d != 256) return KVQ_ERR_BAD_DIM;
-  if ((group != 32 && group != 64 && group != 128 && group != 256) || group > d)
-    return KVQ_ERR_BAD_GROUP;
-  return KVQ_OK;
-}
-
-// Per-device facts, looked up once: SM count and whether the device is
-// compute capability 10.0 (the only one this sm_100a build runs on).
-struct DeviceInfo {
-  int sm_count = 0;
-  bool ok = false;
-};
-
-kvq_status device_info(DeviceInfo* out) {
-  static DeviceInfo info[kMaxDevices];
-  static bool done[kMaxDevices];
-  static std::mutex mu;
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    cudaGetLastError();
-    return KVQ_ERR_CUDA;
-  }
-  std::lock_guard<std::mutex> g(mu);
-  if (!done[dev]) {
-    int major = 0, minor = 0, sms = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return KVQ_ERR_CUDA;
-    }
-    info[dev].sm_count = sms;
-    info[dev].ok = (major == 10 && minor == 0);
-    done[dev] = true;
-  }
-  *out = info[dev];
-  return info[dev].ok ? KVQ_OK : KVQ_ERR_UNSUPPORTED_DEVICE;
-}
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -133,10 +91,6 @@ bool map_s(CUtensorMap* m, const void* base, int d, int group, uint64_t count) {
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 1, base, dims, nullptr, box,
                   CU_TENSOR_MAP_SWIZZLE_NONE);
 }
-
-kvq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
-
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
 bool bits_ok(int32_t d, int32_t bits) {
   return bits == 4 || bits == 6 || bits == 8 || (bits == 3 && d >= 128);
@@ -359,6 +313,8 @@ const char* kvq_status_string(kvq_status s) {
     case KVQ_ERR_BAD_SIZE: return "count or position out of range";
     case KVQ_ERR_DEVICE_TIMEOUT: return "a kernel timed out waiting for its own copy";
     case KVQ_ERR_UNSUPPORTED_DEVICE: return "device is not compute capability 10.0 (sm_100a)";
+    case KVQ_ERR_BAD_INDEX: return "a position, slot, page or length on the device is out of range";
+    case KVQ_ERR_BAD_DTYPE: return "dtype must be KVQ_F16 or KVQ_BF16";
     case KVQ_ERR_BAD_BITS: return "bits must be 3 (d >= 128), 4, 6 or 8";
   }
   return "unknown status";
@@ -376,7 +332,16 @@ kvq_status kvq_device_status(int32_t clear) {
     cudaGetLastError();
     return KVQ_ERR_CUDA;
   }
-  return (v64 | v128 | v256) ? KVQ_ERR_DEVICE_TIMEOUT : KVQ_OK;
+  uint32_t p64 = 0, p128 = 0, p256 = 0;
+  if (kvq::read_paged_status<64>(&p64, clear != 0) != cudaSuccess ||
+      kvq::read_paged_status<128>(&p128, clear != 0) != cudaSuccess ||
+      kvq::read_paged_status<256>(&p256, clear != 0) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_ERR_CUDA;
+  }
+  const uint32_t paged = p64 | p128 | p256;
+  if ((v64 | v128 | v256) || (paged & kvq::kPagedTimeout)) return KVQ_ERR_DEVICE_TIMEOUT;
+  return (paged & kvq::kPagedBadIndex) ? KVQ_ERR_BAD_INDEX : KVQ_OK;
 }
 
 int32_t kvq_version(void) { return 100; }

@@ -1,0 +1,142 @@
+// kvq_paged_inst.cuh -- host-side launchers of the paged-cache kernels of one
+// vector length d.  Included by exactly one translation unit per d
+// (kvq_paged_d64.cu, ...).
+#pragma once
+
+#include <algorithm>
+#include <mutex>
+#include <utility>
+
+#include "kvq_paged.cuh"
+#include "kvq_paged_launch.h"
+
+namespace kvq {
+
+// Status word of this translation unit's kernels, one per device context.
+// Bit 0: a bounded wait ran out; bit 1: an index out of range was skipped.
+static __device__ unsigned g_paged_status;
+
+namespace detail {
+
+// Device address of g_paged_status on the current device (looked up once).
+inline cudaError_t paged_status_ptr(unsigned** out) {
+  constexpr int kMax = 64;
+  static unsigned* ptrs[kMax];
+  static std::mutex mu;
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMax) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> g(mu);
+  if (ptrs[dev] == nullptr) {
+    void* p = nullptr;
+    e = cudaGetSymbolAddress(&p, g_paged_status);
+    if (e != cudaSuccess) return e;
+    ptrs[dev] = static_cast<unsigned*>(p);
+  }
+  *out = ptrs[dev];
+  return cudaSuccess;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_paged(void (*kern)(KArgs...), int64_t grid, int threads, int smem,
+                         cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid), 1, 1);
+  cfg.blockDim = dim3(unsigned(threads), 1, 1);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = KVQ_PDL ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int D, int ROT, int DT>
+cudaError_t append_group(const AppendArgs& a, int group, int sm_count, cudaStream_t stream,
+                         unsigned* st) {
+  const int64_t rows = a.n_tokens * 2 * a.n_heads;
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, int64_t(sm_count) * 12));
+  switch (group) {
+    case 32: return launch_paged(kvq_append_wide_kernel<D, 32, ROT, DT>, grid, kWideThreads, 0, stream, a, st);
+    case 64: return launch_paged(kvq_append_wide_kernel<D, 64, ROT, DT>, grid, kWideThreads, 0, stream, a, st);
+    case 128:
+      if constexpr (D >= 128)
+        return launch_paged(kvq_append_wide_kernel<D, 128, ROT, DT>, grid, kWideThreads, 0, stream, a, st);
+      break;
+    case 256:
+      if constexpr (D >= 256)
+        return launch_paged(kvq_append_wide_kernel<D, 256, ROT, DT>, grid, kWideThreads, 0, stream, a, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <int D, int ROT, int DT>
+cudaError_t attn_simple(const PagedAttnArgs& a, cudaStream_t stream, unsigned* st) {
+  const int64_t rows = a.n_tokens * a.n_kv * a.n_q;
+  return launch_paged(kvq_paged_attn_simple_kernel<D, ROT, DT>, (rows + 3) / 4, kWideThreads, 0,
+                      stream, a, st);
+}
+
+}  // namespace detail
+
+template <int D>
+cudaError_t launch_norm_rope(int dtype, const NormRopeArgs& args, int sm_count,
+                             cudaStream_t stream) {
+  unsigned* st;
+  cudaError_t e = detail::paged_status_ptr(&st);
+  if (e != cudaSuccess) return e;
+  NormRopeArgs a = args;
+  constexpr int RPW = 32 / (D / 8);
+  const int steps = (a.n_rows + RPW - 1) / RPW;  // of a warp over one token
+  // One warp walks over a token's heads (the table row is loaded once) as
+  // long as that leaves 16 warps for every SM; fewer heads a warp otherwise.
+  const int64_t want = int64_t(sm_count) * 16;
+  a.iters = int(std::min<int64_t>(steps, std::max<int64_t>(1, a.n_tokens * steps / want)));
+  a.chunks = (steps + a.iters - 1) / a.iters;
+  const int64_t warps = a.n_tokens * a.chunks;
+  const int64_t grid = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  return dtype == kDtF16
+             ? detail::launch_paged(kvq_norm_rope_kernel<D, kDtF16>, grid, kRopeThreads, 0, stream, a, st)
+             : detail::launch_paged(kvq_norm_rope_kernel<D, kDtBF16>, grid, kRopeThreads, 0, stream, a, st);
+}
+
+template <int D>
+cudaError_t launch_append(int dtype, int rot, int group, const AppendArgs& a, int sm_count,
+                          cudaStream_t stream) {
+  unsigned* st;
+  cudaError_t e = detail::paged_status_ptr(&st);
+  if (e != cudaSuccess) return e;
+  if (rot == kRotSRFT)
+    return dtype == kDtF16 ? detail::append_group<D, kRotSRFT, kDtF16>(a, group, sm_count, stream, st)
+                           : detail::append_group<D, kRotSRFT, kDtBF16>(a, group, sm_count, stream, st);
+  return dtype == kDtF16 ? detail::append_group<D, kRotSRHT, kDtF16>(a, group, sm_count, stream, st)
+                         : detail::append_group<D, kRotSRHT, kDtBF16>(a, group, sm_count, stream, st);
+}
+
+template <int D>
+cudaError_t launch_paged_attn(int dtype, int rot, const PagedAttnArgs& a, int sm_count,
+                              cudaStream_t stream) {
+  unsigned* st;
+  cudaError_t e = detail::paged_status_ptr(&st);
+  if (e != cudaSuccess) return e;
+  if (rot == kRotSRFT)
+    return dtype == kDtF16 ? detail::attn_simple<D, kRotSRFT, kDtF16>(a, stream, st)
+                           : detail::attn_simple<D, kRotSRFT, kDtBF16>(a, stream, st);
+  return dtype == kDtF16 ? detail::attn_simple<D, kRotSRHT, kDtF16>(a, stream, st)
+                         : detail::attn_simple<D, kRotSRHT, kDtBF16>(a, stream, st);
+}
+
+template <int D>
+cudaError_t read_paged_status(uint32_t* value, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_paged_status, sizeof(*value));
+  const uint32_t zero = 0;
+  if (e == cudaSuccess && clear && *value != 0)
+    e = cudaMemcpyToSymbol(g_paged_status, &zero, sizeof(zero));
+  return e;
+}
+
+}  // namespace kvq

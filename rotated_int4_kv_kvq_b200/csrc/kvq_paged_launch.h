@@ -1,0 +1,77 @@
+// kvq_paged_launch.h -- internal interface between the C-ABI front end of the
+// paged cache (kvq_paged_api.cu) and the per-d translation units
+// (kvq_paged_d64.cu, ...).  Not part of the public API.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace kvq {
+
+constexpr int kDtF16 = 0, kDtBF16 = 1;  // kvq_dtype
+
+// Bits of the paged kernels' status words.
+constexpr unsigned kPagedTimeout = 1u, kPagedBadIndex = 2u;
+
+struct RopeTable {
+  const float* cos_sin;  // [n_pos][rot_dim], or NULL
+  int64_t n_pos;
+  int rot_dim;
+  int interleaved;
+  float eps;
+};
+
+struct NormRopeArgs {
+  const uint16_t *q, *k;
+  uint16_t *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;  // elements per token
+  const int32_t* positions;
+  const float *q_weight, *k_weight;
+  RopeTable rope;
+  int64_t n_tokens;
+  int n_heads, n_rows;  // query heads; query and key heads
+  int iters;            // steps of a warp over a token's heads
+  int chunks;           // warps per token
+};
+
+struct AppendArgs {
+  const uint16_t *k, *v;
+  int64_t k_stride, v_stride;
+  const int64_t* slots;
+  const int32_t* positions;
+  const float* k_weight;  // NULL: no norm
+  RopeTable rope;
+  uint8_t *k_packed, *v_packed;
+  float *k_scales, *v_scales;
+  const int8_t* signs;
+  uint16_t *k_hat, *v_hat;  // NULL: not wanted
+  int64_t n_tokens, n_slots;
+  int n_heads, page_shift;
+};
+
+struct PagedAttnArgs {
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t q_stride, out_stride;
+  const int32_t *cu_q, *kv_len, *page_table;
+  const uint8_t *k_packed, *v_packed;
+  const float *k_scales, *v_scales;
+  const int8_t* signs;
+  int64_t n_tokens, n_pages, max_pages;
+  int n_seqs, n_kv, n_q, page_shift, group, window;
+  float qscale;  // sm_scale * log2(e)
+};
+
+// Implemented once per d in the matching translation unit.
+template <int D>
+cudaError_t launch_norm_rope(int dtype, const NormRopeArgs& a, int sm_count, cudaStream_t stream);
+template <int D>
+cudaError_t launch_append(int dtype, int rot, int group, const AppendArgs& a, int sm_count,
+                          cudaStream_t stream);
+template <int D>
+cudaError_t launch_paged_attn(int dtype, int rot, const PagedAttnArgs& a, int sm_count,
+                              cudaStream_t stream);
+template <int D>
+cudaError_t read_paged_status(uint32_t* value, bool clear);
+
+}  // namespace kvq

@@ -146,19 +146,14 @@ __device__ __forceinline__ void dft_small(f2 (&z)[C]) {
 }
 
 // Forward rotation: Y (the lane's W values of chunk k2, unnormalized,
-// y = KAPPA * Y) from the lane's sign-flipped fp16 words.
+// y = KAPPA * Y) from the lane's sign-flipped pairs (consumed).
 template <int D, int ROT>
-__device__ __forceinline__ void wide_rotate_fwd(const uint32_t (&xw)[Wide<D, ROT>::C],
+__device__ __forceinline__ void wide_rotate_fwd(f2 (&z)[Wide<D, ROT>::C],
                                                 const WideLane<D, ROT>& L,
                                                 float (&Y)[Wide<D, ROT>::W]) {
   using P = Wide<D, ROT>;
   if constexpr (ROT == kRotSRHT) {
-    f2 v[P::C];
-#pragma unroll
-    for (int j = 0; j < P::C; ++j) {
-      const float2 f = half2_bits_to_float2(xw[j]);
-      v[j] = mk2(f.x, f.y);
-    }
+    f2 (&v)[P::C] = z;
     fwht<P::C>(v);
 #pragma unroll
     for (int b = 1; b < 32; b <<= 1) {
@@ -173,12 +168,6 @@ __device__ __forceinline__ void wide_rotate_fwd(const uint32_t (&xw)[Wide<D, ROT
       Y[2 * j + 1] = hi2(v[j]);
     }
   } else {
-    f2 z[P::C];
-#pragma unroll
-    for (int j = 0; j < P::C; ++j) {
-      const float2 f = half2_bits_to_float2(xw[j]);
-      z[j] = mk2(f.x, f.y);
-    }
     dft_small<P::C, false>(z);
 #pragma unroll
     for (int k1 = 1; k1 < P::C; ++k1) z[k1] = cmulw(z[k1], L.s2[k1]);
@@ -214,15 +203,30 @@ __device__ __forceinline__ void wide_rotate_fwd(const uint32_t (&xw)[Wide<D, ROT
   }
 }
 
-// Inverse rotation: the lane's fp16 words (before the sign flip) of
+// The same from the lane's sign-flipped fp16 words.
+template <int D, int ROT>
+__device__ __forceinline__ void wide_rotate_fwd(const uint32_t (&xw)[Wide<D, ROT>::C],
+                                                const WideLane<D, ROT>& L,
+                                                float (&Y)[Wide<D, ROT>::W]) {
+  using P = Wide<D, ROT>;
+  f2 z[P::C];
+#pragma unroll
+  for (int j = 0; j < P::C; ++j) {
+    const float2 f = half2_bits_to_float2(xw[j]);
+    z[j] = mk2(f.x, f.y);
+  }
+  wide_rotate_fwd<D, ROT>(z, L, Y);
+}
+
+// Inverse rotation: the lane's pairs (before the sign flip) of
 // u = R^T y_hat from Yin = KAPPA * y_hat (the lane's chunk k2).
 template <int D, int ROT>
 __device__ __forceinline__ void wide_rotate_inv(const float (&Y)[Wide<D, ROT>::W],
                                                 const WideLane<D, ROT>& L,
-                                                uint32_t (&xw)[Wide<D, ROT>::C]) {
+                                                f2 (&z)[Wide<D, ROT>::C]) {
   using P = Wide<D, ROT>;
   if constexpr (ROT == kRotSRHT) {
-    f2 v[P::C];
+    f2 (&v)[P::C] = z;
 #pragma unroll
     for (int j = 0; j < P::C; ++j) v[j] = mk2(Y[2 * j], Y[2 * j + 1]);
 #pragma unroll
@@ -233,8 +237,6 @@ __device__ __forceinline__ void wide_rotate_inv(const float (&Y)[Wide<D, ROT>::W
       for (int j = 0; j < P::C; ++j) v[j] = fma2(sg2, v[j], shfl_xor2(v[j], b));
     }
     fwht<P::C>(v);
-#pragma unroll
-    for (int j = 0; j < P::C; ++j) xw[j] = float2_to_half2_bits(lo2(v[j]), hi2(v[j]));
   } else {
     f2 x[P::C];
 #pragma unroll
@@ -243,7 +245,6 @@ __device__ __forceinline__ void wide_rotate_inv(const float (&Y)[Wide<D, ROT>::W
     part[0] = shfl_idx2(x[0], L.src0);
 #pragma unroll
     for (int k1 = 1; k1 < P::C; ++k1) part[k1] = shfl_xor2(x[P::C - k1], 31);
-    f2 z[P::C];
 #pragma unroll
     for (int k1 = 0; k1 < P::C; ++k1) {
       // Q_k = S + i W_d^{-k} D, S = A + conj B', D = A - conj B'
@@ -274,9 +275,19 @@ __device__ __forceinline__ void wide_rotate_inv(const float (&Y)[Wide<D, ROT>::W
 #pragma unroll
     for (int k1 = 1; k1 < P::C; ++k1) z[k1] = cmulwc(z[k1], L.s2[k1]);
     dft_small<P::C, true>(z);
-#pragma unroll
-    for (int j = 0; j < P::C; ++j) xw[j] = float2_to_half2_bits(lo2(z[j]), hi2(z[j]));
   }
+}
+
+// The same as fp16 words.
+template <int D, int ROT>
+__device__ __forceinline__ void wide_rotate_inv(const float (&Y)[Wide<D, ROT>::W],
+                                                const WideLane<D, ROT>& L,
+                                                uint32_t (&xw)[Wide<D, ROT>::C]) {
+  using P = Wide<D, ROT>;
+  f2 z[P::C];
+  wide_rotate_inv<D, ROT>(Y, L, z);
+#pragma unroll
+  for (int j = 0; j < P::C; ++j) xw[j] = float2_to_half2_bits(lo2(z[j]), hi2(z[j]));
 }
 
 // ------------------------------------------------------ decode kernel ---
@@ -391,18 +402,15 @@ __device__ __forceinline__ uint32_t wide_load_code(const uint8_t* qrow, const Wi
   }
 }
 
-// Forward step on one fp16 row (steps a1-a5): writes the row's codes and
-// scales, returns this lane's code bytes and its group's scale.
-template <int D, int G, int ROT, bool RO = true>
-__device__ __forceinline__ void wide_quantize_row(const uint16_t* src, uint8_t* qrow, float* srow,
-                                                  const WideLane<D, ROT>& L, uint32_t& code,
-                                                  float& s) {
+// Quantizes a rotated row (steps a3-a5): writes its codes and scales, returns
+// this lane's code bytes and its group's scale.
+template <int D, int G, int ROT>
+__device__ __forceinline__ void wide_quantize_rotated(const float (&Y)[Wide<D, ROT>::W],
+                                                      uint8_t* qrow, float* srow,
+                                                      const WideLane<D, ROT>& L, uint32_t& code,
+                                                      float& s) {
   using P = Wide<D, ROT>;
   constexpr int GL = G / P::W;  // lanes (chunks) per group
-  uint32_t xw[P::C];
-  wide_load_words<D, ROT, RO>(src, L, xw);
-  float Y[P::W];
-  wide_rotate_fwd<D, ROT>(xw, L, Y);
   float m = fabsf(Y[0]);
 #pragma unroll
   for (int j = 1; j < P::W; ++j) m = fmaxf(m, fabsf(Y[j]));
@@ -419,26 +427,44 @@ __device__ __forceinline__ void wide_quantize_row(const uint16_t* src, uint8_t* 
   if (L.k2 % GL == 0) srow[L.k2 / GL] = s;
 }
 
+// Forward step on one fp16 row (steps a1-a5).
+template <int D, int G, int ROT, bool RO = true>
+__device__ __forceinline__ void wide_quantize_row(const uint16_t* src, uint8_t* qrow, float* srow,
+                                                  const WideLane<D, ROT>& L, uint32_t& code,
+                                                  float& s) {
+  using P = Wide<D, ROT>;
+  uint32_t xw[P::C];
+  wide_load_words<D, ROT, RO>(src, L, xw);
+  float Y[P::W];
+  wide_rotate_fwd<D, ROT>(xw, L, Y);
+  wide_quantize_rotated<D, G, ROT>(Y, qrow, srow, L, code, s);
+}
+
+// The lane's values KAPPA s q from its code bytes and scale (step a6).
+template <int D, int ROT>
+__device__ __forceinline__ void wide_dequant(uint32_t code, float s, float (&Y)[Wide<D, ROT>::W]) {
+  using P = Wide<D, ROT>;
+  const f2 magic = mk2(kUnpackMagic, kUnpackMagic);
+  f2 q[4];
+  unpack8(code, q);
+  const float sk = s * P::KAPPA;
+  const f2 sk2 = mk2(sk, sk);
+#pragma unroll
+  for (int j = 0; j < P::C; ++j) {
+    const f2 v = mul2(sub2(q[j], magic), sk2);
+    Y[2 * j] = lo2(v);
+    Y[2 * j + 1] = hi2(v);
+  }
+}
+
 // Inverse step on one row (steps a6-a7) from the lane's code bytes and
 // scale; writes the fp16 row.
 template <int D, int ROT>
 __device__ __forceinline__ void wide_dequant_row(uint32_t code, float s, uint16_t* dst,
                                                  const WideLane<D, ROT>& L) {
   using P = Wide<D, ROT>;
-  const f2 magic = mk2(kUnpackMagic, kUnpackMagic);
   float Y[P::W];
-  {
-    f2 q[4];
-    unpack8(code, q);
-    const float sk = s * P::KAPPA;
-    const f2 sk2 = mk2(sk, sk);
-#pragma unroll
-    for (int j = 0; j < P::C; ++j) {
-      const f2 v = mul2(sub2(q[j], magic), sk2);
-      Y[2 * j] = lo2(v);
-      Y[2 * j + 1] = hi2(v);
-    }
-  }
+  wide_dequant<D, ROT>(code, s, Y);
   uint32_t xo[P::C];
   wide_rotate_inv<D, ROT>(Y, L, xo);
   wide_store_words<D, ROT>(dst, L, xo);

@@ -23,7 +23,7 @@ STATUS = {
     0: "KVQ_OK", 1: "KVQ_ERR_NULL", 2: "KVQ_ERR_BAD_DIM", 3: "KVQ_ERR_BAD_GROUP",
     4: "KVQ_ERR_MISALIGNED", 5: "KVQ_ERR_BAD_ROT", 6: "KVQ_ERR_CUDA",
     7: "KVQ_ERR_BAD_SIZE", 8: "KVQ_ERR_DEVICE_TIMEOUT", 9: "KVQ_ERR_UNSUPPORTED_DEVICE",
-    10: "KVQ_ERR_BAD_BITS",
+    10: "KVQ_ERR_BAD_BITS", 11: "KVQ_ERR_BAD_INDEX", 12: "KVQ_ERR_BAD_DTYPE",
 }
 
 LIB_PATH = os.environ.get("KVQ_LIBRARY") or os.path.join(
@@ -32,7 +32,25 @@ LIB_PATH = os.environ.get("KVQ_LIBRARY") or os.path.join(
 EXPORTS = ("kvq_rot_quant_fwd", "kvq_dequant_rot_inv", "kvq_rot_quant_fwd_lambda",
            "kvq_dequant_rot_inv_lambda", "kvq_rot_quant_fwd_bits", "kvq_dequant_rot_inv_bits",
            "kvq_decode_step", "kvq_decode_step_windowed",
-           "kvq_attend_decode", "kvq_status_string", "kvq_device_status", "kvq_version")
+           "kvq_attend_decode", "kvq_qk_norm_rope", "kvq_paged_append", "kvq_paged_attend",
+           "kvq_paged_attend_workspace", "kvq_status_string", "kvq_device_status", "kvq_version")
+
+DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # kvq_dtype
+PAGE_SIZES = (16, 32, 64, 128, 256)
+
+
+class _PagedCacheC(ctypes.Structure):  # kvq_paged_cache
+    _fields_ = [("k_packed", ctypes.c_void_p), ("v_packed", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("n_kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("d", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("signs", ctypes.c_void_p), ("rot", ctypes.c_int32)]
+
+
+class _RopeC(ctypes.Structure):  # kvq_rope
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("n_pos", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 class KVQError(RuntimeError):
@@ -67,6 +85,16 @@ def _load() -> ctypes.CDLL:
     lib.kvq_attend_decode.argtypes = [p, p, p, p, p, i64, i32, i64, i64, i32, i32, p, i32,
                                       ctypes.c_float, p, p]
     lib.kvq_attend_decode.restype = i32
+    lib.kvq_qk_norm_rope.argtypes = [p, p, i32, i64, i32, i32, i32, i64, i64, p, p, p, p, p, p,
+                                     i64, i64, p]
+    lib.kvq_qk_norm_rope.restype = i32
+    lib.kvq_paged_append.argtypes = [p, p, i32, i64, i64, i64, p, p, p, p, p, p, p, p]
+    lib.kvq_paged_append.restype = i32
+    lib.kvq_paged_attend.argtypes = [p, i32, i64, i64, p, p, p, p, i64, i64, i32, i32, i32,
+                                     ctypes.c_float, p, i64, p, i64, p]
+    lib.kvq_paged_attend.restype = i32
+    lib.kvq_paged_attend_workspace.argtypes = [i64, i32, i32, i32, i32]
+    lib.kvq_paged_attend_workspace.restype = i64
     lib.kvq_status_string.argtypes = [i32]
     lib.kvq_status_string.restype = ctypes.c_char_p
     lib.kvq_device_status.argtypes = [i32]
@@ -125,6 +153,17 @@ def _current(dev: torch.device):
     if dev.index is None or dev.index == torch.cuda.current_device():
         return contextlib.nullcontext()
     return torch.cuda.device(dev)
+
+
+def _on(stream, dev: torch.device):
+    """Context in which tensors allocated for a call belong to the stream the
+    call runs on: memory that the current stream's queued work still uses is
+    not handed to a kernel of another stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
 
 
 def _check(t: torch.Tensor, name: str, dtype, shape):
@@ -318,6 +357,230 @@ def kvq_attend_decode(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.T
                                    _ptr(v_scales), h, nq, cap, length, d, group, _ptr(signs),
                                    rot, scale, _ptr(out), _stream(stream, dev))
     _raise("kvq_attend_decode", st)
+    return out
+
+
+def rope_table(n_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Table [n_pos, rot_dim] f32 of the position rotation: row p holds the
+    rot_dim/2 cosines, then the sines, of p theta^(-2i/rot_dim).  The angles
+    are formed in 64 bits: at far positions 32 lose the fraction of a turn."""
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+    p = torch.arange(n_pos, dtype=torch.float64, device=device)
+    angle = p[:, None] * theta ** (-i / rot_dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def paged_rows(cu_q: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+               page_size: int, n_tokens: int):
+    """Positions [n_tokens] int32 and slots [n_tokens] int64 of the new tokens
+    that cu_q, kv_len (after the append) and page_table describe, for
+    kvq_qk_norm_rope and kvq_paged_append; -1 for tokens of no sequence.  The
+    same for every layer: computed once a step, on the device, without a
+    synchronization."""
+    tok = torch.arange(n_tokens, device=cu_q.device)
+    seq = torch.searchsorted(cu_q[1:], tok, right=True).clamp_(max=kv_len.shape[0] - 1)
+    here = (tok >= cu_q[0]) & (tok < cu_q[-1])
+    pos = torch.where(here, kv_len[seq].long() - cu_q[1:][seq] + tok, -1)
+    page = page_table[seq, (pos // page_size).clamp_(0, page_table.shape[1] - 1)].long()
+    slots = torch.where(pos >= 0, page * page_size + pos % page_size, -1)
+    return pos.int(), slots
+
+
+class PagedCache:
+    """The int4 K/V cache of one layer in pages: k_packed, v_packed
+    [pages, H, page_size, d/2] u8, k_scales, v_scales [pages, H, page_size,
+    d/group] f32, the sign vector [d] i8 and the rotation.  A page row is a row
+    of kvq_rot_quant_fwd."""
+
+    def __init__(self, k_packed: torch.Tensor, k_scales: torch.Tensor, v_packed: torch.Tensor,
+                 v_scales: torch.Tensor, signs: torch.Tensor, rot: int = SRFT):
+        if not isinstance(k_packed, torch.Tensor) or k_packed.dim() != 4:
+            raise ValueError("k_packed must be a tensor [pages, heads, page_size, d/2]")
+        if not isinstance(k_scales, torch.Tensor) or k_scales.dim() != 4 or k_scales.shape[3] < 1:
+            raise ValueError("k_scales must be a tensor [pages, heads, page_size, d/group]")
+        self.n_pages, self.n_kv_heads, self.page_size, half = k_packed.shape
+        self.d = 2 * half
+        self.group = self.d // k_scales.shape[3]
+        self.rot = rot
+        for name, t in (("k_packed", k_packed), ("v_packed", v_packed)):
+            _check(t, name, torch.uint8, k_packed.shape)
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _check(t, name, torch.float32, (*k_packed.shape[:3], self.d // max(self.group, 1)))
+        _check(signs, "signs", torch.int8, (self.d,))
+        self.k_packed, self.k_scales = k_packed, k_scales
+        self.v_packed, self.v_scales = v_packed, v_scales
+        self.signs = signs
+        self.c = _PagedCacheC(_ptr(k_packed), _ptr(v_packed), _ptr(k_scales), _ptr(v_scales),
+                              self.n_pages, self.n_kv_heads, self.page_size, self.d, self.group,
+                              _ptr(signs), rot)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, d: int, group: int,
+              signs: torch.Tensor, rot: int = SRFT) -> "PagedCache":
+        """A pool of n_pages uninitialized pages on the device of `signs`."""
+        def codes():
+            return torch.empty((n_pages, n_kv_heads, page_size, d // 2), dtype=torch.uint8,
+                               device=signs.device)
+
+        def scales():
+            return torch.empty((n_pages, n_kv_heads, page_size, d // group), device=signs.device)
+        return cls(codes(), scales(), codes(), scales(), signs, rot)
+
+    def tensors(self):
+        return self.k_packed, self.k_scales, self.v_packed, self.v_scales, self.signs
+
+
+def _check_tokens(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Checks rows [tokens, heads, d] whose tokens may lie apart (a part of a
+    fused projection); returns the token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or dtype not in DTYPES:
+        raise TypeError(f"{name} must be {dtype if dtype in DTYPES else 'float16 or bfloat16'}, "
+                        f"got {t.dtype}")
+    if t.shape != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    heads, d = shape[1], shape[2]
+    if t.shape[0] <= 1:  # the stride of a single token says nothing
+        if heads * d and not (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)):
+            raise ValueError(f"the heads of a token of {name} must be contiguous")
+        return heads * d
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0)
+
+
+def _rope(positions, cos_sin, interleaved, eps, n_tokens):
+    rot_dim = n_pos = 0
+    if cos_sin is not None:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _check(positions, "positions", torch.int32, (n_tokens,))
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be a table [positions, rot_dim]")
+        _check(cos_sin, "cos_sin", torch.float32, cos_sin.shape)
+        n_pos, rot_dim = cos_sin.shape
+    return _RopeC(_ptr(cos_sin), n_pos, rot_dim, 1 if interleaved else 0, eps)
+
+
+def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *,
+                     positions: torch.Tensor | None = None, cos_sin: torch.Tensor | None = None,
+                     interleaved: bool = False, q_weight: torch.Tensor | None = None,
+                     k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                     q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                     stream=None):
+    """Norm (weights [d] f32; none without a weight) and position rotation
+    (table cos_sin [positions, rot_dim] f32, see rope_table; none without a
+    table) of queries q [T, Hq, d] and keys k [T, Hk, d], fp16 or bf16, in one
+    pass.  Returns (q_out, k_out), allocated when not given; they may be q and
+    k themselves.  Rows of tokens at negative positions are left as they were."""
+    t, hq, d = q.shape
+    qs = _check_tokens(q, "q", q.dtype, (t, hq, d))
+    if q_out is None:
+        with _on(stream, q.device):
+            q_out = torch.empty((t, hq, d), dtype=q.dtype, device=q.device)
+    qos = _check_tokens(q_out, "q_out", q.dtype, (t, hq, d))
+    hk = ks = kos = 0
+    if k is not None:
+        hk = k.shape[1]
+        ks = _check_tokens(k, "k", q.dtype, (t, hk, d))
+        if k_out is None:
+            with _on(stream, q.device):
+                k_out = torch.empty((t, hk, d), dtype=q.dtype, device=q.device)
+        kos = _check_tokens(k_out, "k_out", q.dtype, (t, hk, d))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check(w, name, torch.float32, (d,))
+    rope = _rope(positions, cos_sin, interleaved, eps, t)
+    dev = _device_of((q, k, positions if cos_sin is not None else None, cos_sin, q_weight,
+                      k_weight, q_out, k_out), stream)
+    with _current(dev):
+        st = lib.kvq_qk_norm_rope(_ptr(q), _ptr(k), DTYPES[q.dtype], t, hq, hk, d, qs, ks,
+                                  _ptr(positions), _ptr(q_weight), _ptr(k_weight),
+                                  ctypes.byref(rope), _ptr(q_out), _ptr(k_out), qos, kos,
+                                  _stream(stream, dev))
+    _raise("kvq_qk_norm_rope", st)
+    return q_out, k_out
+
+
+def kvq_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: PagedCache, *,
+                     positions: torch.Tensor | None = None, cos_sin: torch.Tensor | None = None,
+                     interleaved: bool = False, k_weight: torch.Tensor | None = None,
+                     eps: float = 1e-6, k_hat: torch.Tensor | None = None,
+                     v_hat: torch.Tensor | None = None, stream=None) -> None:
+    """Writes the new tokens' k, v [T, H, d] (fp16 or bf16) as rows `slots`
+    [T] i64 (page * page_size + row in the page; negative: padding) of the
+    cache, k after its norm and position rotation (as in kvq_qk_norm_rope).
+    k_hat, v_hat [T, H, d], when given, receive the values the new rows stand
+    for."""
+    t = k.shape[0]
+    shape = (t, cache.n_kv_heads, cache.d)
+    ks = _check_tokens(k, "k", k.dtype, shape)
+    vs = _check_tokens(v, "v", k.dtype, shape)
+    _check(slots, "slots", torch.int64, (t,))
+    if k_weight is not None:
+        _check(k_weight, "k_weight", torch.float32, (cache.d,))
+    for name, x in (("k_hat", k_hat), ("v_hat", v_hat)):
+        if x is not None:
+            _check(x, name, k.dtype, shape)
+    rope = _rope(positions, cos_sin, interleaved, eps, t)
+    dev = _device_of((k, v, slots, positions if cos_sin is not None else None, cos_sin, k_weight,
+                      k_hat, v_hat, *cache.tensors()), stream)
+    with _current(dev):
+        st = lib.kvq_paged_append(_ptr(k), _ptr(v), DTYPES[k.dtype], t, ks, vs, _ptr(slots),
+                                  _ptr(positions), _ptr(k_weight), ctypes.byref(rope),
+                                  ctypes.byref(cache.c), _ptr(k_hat), _ptr(v_hat),
+                                  _stream(stream, dev))
+    _raise("kvq_paged_append", st)
+
+
+def kvq_paged_attend(q: torch.Tensor, cache: PagedCache, cu_q: torch.Tensor,
+                     kv_len: torch.Tensor, page_table: torch.Tensor, *, max_q_len: int,
+                     window: int = 0, sm_scale: float | None = None,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Causal attention of new tokens q [T, H * n_q, d] (fp16 or bf16) over
+    the paged cache, which holds their keys and values already.  cu_q [S+1]
+    i32: first token of each sequence; kv_len [S] i32: its cached rows;
+    page_table [S, max_pages] i32; max_q_len: the most new tokens of a sequence
+    (chooses the kernel); window: attend at most that many rows (0: all);
+    sm_scale defaults to 1/sqrt(d).  Returns out [T, H * n_q, d]; rows of no
+    sequence are left as they were.  The workspace (uint8) is allocated when
+    not given; one that is given must not be used by another call before this
+    one has finished on the device."""
+    t, h, d = q.shape
+    if d != cache.d or h % cache.n_kv_heads != 0 or h == 0:
+        raise ValueError(f"q [{t}, {h}, {d}] does not fit a cache of {cache.n_kv_heads} KV heads "
+                         f"and d = {cache.d}")
+    qs = _check_tokens(q, "q", q.dtype, (t, h, d))
+    if out is None:
+        with _on(stream, q.device):
+            out = torch.empty((t, h, d), dtype=q.dtype, device=q.device)
+    os_ = _check_tokens(out, "out", q.dtype, (t, h, d))
+    n_seqs = kv_len.shape[0]
+    _check(kv_len, "kv_len", torch.int32, (n_seqs,))
+    _check(cu_q, "cu_q", torch.int32, (n_seqs + 1,))
+    _check(page_table, "page_table", torch.int32, (n_seqs, page_table.shape[-1]))
+    scale = float(sm_scale) if sm_scale is not None else d ** -0.5
+    n_q = h // cache.n_kv_heads
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    dev = _device_of((q, out, cu_q, kv_len, page_table, workspace, *cache.tensors()), stream)
+    with _current(dev):
+        if workspace is None:
+            need = lib.kvq_paged_attend_workspace(t, cache.n_kv_heads, n_q, d, max_q_len)
+            if need < 0:
+                _raise("kvq_paged_attend_workspace", -need)
+            if need > 0:
+                with _on(stream, dev):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        st = lib.kvq_paged_attend(_ptr(q), DTYPES[q.dtype], t, qs, ctypes.byref(cache.c),
+                                  _ptr(cu_q), _ptr(kv_len), _ptr(page_table), n_seqs,
+                                  page_table.shape[1], n_q, max_q_len, window, scale, _ptr(out),
+                                  os_, _ptr(workspace),
+                                  0 if workspace is None else workspace.numel(),
+                                  _stream(stream, dev))
+    _raise("kvq_paged_attend", st)
     return out
 
 
