@@ -129,80 +129,4 @@ __global__ void __launch_bounds__(kWideThreads) kvq_append_wide_kernel(const App
   pdl_release();
 }
 
-// ------------------------------------------------- attention, one row a warp ---
-
-// A warp per (token, query head): scores by a shuffle reduction per row.
-template <int D, int ROT, int DT>
-__global__ void __launch_bounds__(kWideThreads) kvq_paged_attn_simple_kernel(const PagedAttnArgs a,
-                                                                             unsigned* status) {
-  using P = Wide<D, ROT>;
-  const int lane = threadIdx.x & 31;
-  const int64_t gw = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  pdl_wait();
-  const int heads = a.n_kv * a.n_q;
-  const int64_t tok = gw / heads;
-  const int h = int(gw - tok * heads), kvh = h / a.n_q;
-  if (tok >= a.n_tokens) return;
-  int lo = -1;
-  int64_t c0 = 0, c1 = 0, len = 0;
-  for (int s = 0; s < a.n_seqs; ++s) {
-    const int64_t b = __ldg(a.cu_q + s), e = __ldg(a.cu_q + s + 1), n = __ldg(a.kv_len + s);
-    if (b < 0 || e < b || e > a.n_tokens || n < 0 || n > (a.max_pages << a.page_shift)) {
-      if (lane == 0) flag_bad_index(status);
-    } else if (tok >= b && tok < e) {
-      lo = s, c0 = b, c1 = e, len = n;
-    }
-  }
-  if (lo < 0) return;  // rows of no sequence
-  WideLane<D, ROT> L;
-  L.init(a.signs, lane);
-  const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + tok * a.q_stride + int64_t(h) * D);
-  f2 z[P::C];
-#pragma unroll
-  for (int j = 0; j < P::C; ++j) {
-    const float2 f = pair_to_float2<DT>(__ldg(src + wide_word<D, ROT>(lane, j)) ^ L.mask[j]);
-    z[j] = mk2(f.x, f.y);
-  }
-  float Q[P::W], acc[P::W];
-  wide_rotate_fwd<D, ROT>(z, L, Q);
-#pragma unroll
-  for (int w = 0; w < P::W; ++w) Q[w] *= P::KAPPA * a.qscale, acc[w] = 0.0f;
-  const int64_t p = len - (c1 - c0) + (tok - c0);
-  const int64_t t0 = a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0;
-  const int grp = L.k2 * P::W / a.group, ng = D / a.group;
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t t = t0; t <= p; ++t) {
-    const int64_t page = __ldg(a.page_table + lo * a.max_pages + (t >> a.page_shift));
-    if (page < 0 || page >= a.n_pages) {
-      if (lane == 0) flag_bad_index(status);
-      continue;
-    }
-    const int64_t row = ((page * a.n_kv + kvh) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-    float Y[P::W];
-    wide_dequant<D, ROT>(wide_load_code<D, ROT>(a.k_packed + row * (D / 2), L),
-                         __ldg(a.k_scales + row * ng + grp), Y);
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < P::W; ++w) s = fmaf(Q[w], Y[w], s);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(kFull, s, o);
-    s *= 1.0f / P::KAPPA;
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), e = exp2f(s - mn);
-    wide_dequant<D, ROT>(wide_load_code<D, ROT>(a.v_packed + row * (D / 2), L),
-                         __ldg(a.v_scales + row * ng + grp), Y);
-    l = fmaf(l, f, e);
-    m = mn;
-#pragma unroll
-    for (int w = 0; w < P::W; ++w) acc[w] = fmaf(acc[w], f, e * Y[w]);
-  }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-  for (int w = 0; w < P::W; ++w) acc[w] *= inv;  // KAPPA is in already
-  wide_rotate_inv<D, ROT>(acc, L, z);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + tok * a.out_stride + int64_t(h) * D);
-#pragma unroll
-  for (int j = 0; j < P::C; ++j)
-    dst[wide_word<D, ROT>(lane, j)] = float2_to_pair<DT>(lo2(z[j]), hi2(z[j])) ^ L.mask[j];
-}
-
 }  // namespace kvq

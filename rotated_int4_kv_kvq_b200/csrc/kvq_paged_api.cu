@@ -167,7 +167,7 @@ int64_t kvq_paged_attend_workspace(int64_t n_tokens, int32_t n_kv_heads, int32_t
   if (n_tokens < 0 || n_tokens > kMaxRows || n_kv_heads < 1 || n_q < 1 || n_q > 64 ||
       int64_t(n_kv_heads) * n_q > 65535 || n_tokens * n_kv_heads * n_q > kMaxRows || max_q_len < 1)
     return -KVQ_ERR_BAD_SIZE;
-  return 0;
+  return kvq::few_rows_workspace(d, int64_t(max_q_len) * n_q);
 }
 
 kvq_status kvq_paged_attend(const void* q, kvq_dtype dtype, int64_t n_tokens, int64_t q_stride,
@@ -217,14 +217,17 @@ kvq_status kvq_paged_attend(const void* q, kvq_dtype dtype, int64_t n_tokens, in
   a.n_kv = cache->n_kv_heads;
   a.n_q = n_q;
   a.page_shift = log2_page(cache->page_size);
+  a.d = cache->d;
   a.group = cache->group;
+  a.dtype = dtype;
+  a.rot = cache->rot;
+  a.workspace = static_cast<uint8_t*>(workspace);
   a.window = window;
   a.qscale = sm_scale * kLog2e;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int rot = cache->rot;
-  return from_cuda(cache->d == 64    ? kvq::launch_paged_attn<64>(dtype, rot, a, dev.sm_count, st)
-                   : cache->d == 128 ? kvq::launch_paged_attn<128>(dtype, rot, a, dev.sm_count, st)
-                                     : kvq::launch_paged_attn<256>(dtype, rot, a, dev.sm_count, st));
+  return from_cuda(cache->d == 64    ? kvq::launch_paged_attn<64>(a, max_q_len, dev.sm_count, st)
+                   : cache->d == 128 ? kvq::launch_paged_attn<128>(a, max_q_len, dev.sm_count, st)
+                                     : kvq::launch_paged_attn<256>(a, max_q_len, dev.sm_count, st));
 }
 
 }  // extern "C"

@@ -8,6 +8,7 @@
 #include <utility>
 
 #include "kvq_paged.cuh"
+#include "kvq_pdecode.cuh"
 #include "kvq_paged_launch.h"
 
 namespace kvq {
@@ -74,11 +75,67 @@ cudaError_t append_group(const AppendArgs& a, int group, int sm_count, cudaStrea
   return cudaErrorInvalidValue;
 }
 
-template <int D, int ROT, int DT>
-cudaError_t attn_simple(const PagedAttnArgs& a, cudaStream_t stream, unsigned* st) {
-  const int64_t rows = a.n_tokens * a.n_kv * a.n_q;
-  return launch_paged(kvq_paged_attn_simple_kernel<D, ROT, DT>, (rows + 3) / 4, kWideThreads, 0,
-                      stream, a, st);
+// Resident blocks per SM of an attention kernel, its shared memory opted into
+// (looked up once per kernel and device).
+template <auto Kern>
+cudaError_t paged_occupancy(int threads, int smem, int* out) {
+  constexpr int kMax = 64;
+  static int occ[kMax];
+  static std::mutex mu;
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMax) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> g(mu);
+  if (occ[dev] == 0) {
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    int b = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, Kern, threads, smem);
+    if (e != cudaSuccess) return e;
+    occ[dev] = std::max(b, 1);
+  }
+  *out = occ[dev];
+  return cudaSuccess;
+}
+
+template <int D, int R, int NG>
+cudaError_t few_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t stream, unsigned* st) {
+  using C = Pd<D, R, NG>;
+  constexpr auto kern = kvq_paged_decode_kernel<D, R, NG>;
+  int occ;
+  cudaError_t e = paged_occupancy<kern>(kPdThreads, C::SMEM, &occ);
+  if (e != cudaSuccess) return e;
+  // no more blocks than there can be units, or than can be resident at once
+  // (in shared and in tensor memory)
+  const int64_t items = (args.n_tokens * args.n_q + R - 1) / R + args.n_seqs;
+  const int64_t tiles = (args.max_pages << args.page_shift) / C::KT + 1;
+  int64_t grid = std::min<int64_t>(int64_t(sm_count) * std::min(occ, 512 / C::TMEM), kMaxBlocks);
+  if (items * args.n_kv < grid) grid = std::min<int64_t>(grid, items * args.n_kv * std::min<int64_t>(tiles, grid));
+  PagedAttnArgs a = args;
+  static_assert(sizeof(JoinInfo) <= 32, "workspace");
+  a.join = reinterpret_cast<JoinInfo*>(a.workspace);
+  a.parts = reinterpret_cast<float*>(a.workspace + kMaxBlocks * 32);
+  e = launch_paged(kern, grid, kPdThreads, C::SMEM, stream, a, st);
+  if (e != cudaSuccess) return e;
+  return a.rot == kRotSRFT
+             ? launch_paged(kvq_paged_join_kernel<D, R, kRotSRFT>, grid, 256, 0, stream, a)
+             : launch_paged(kvq_paged_join_kernel<D, R, kRotSRHT>, grid, 256, 0, stream, a);
+}
+
+template <int D, int R>
+cudaError_t few_rows_group(const PagedAttnArgs& a, int sm_count, cudaStream_t stream,
+                           unsigned* st) {
+  switch (D / a.group) {
+    case 1: return few_rows<D, R, 1>(a, sm_count, stream, st);
+    case 2: return few_rows<D, R, 2>(a, sm_count, stream, st);
+    case 4:
+      if constexpr (D >= 128) return few_rows<D, R, 4>(a, sm_count, stream, st);
+      break;
+    case 8:
+      if constexpr (D >= 256) return few_rows<D, R, 8>(a, sm_count, stream, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace detail
@@ -118,16 +175,14 @@ cudaError_t launch_append(int dtype, int rot, int group, const AppendArgs& a, in
 }
 
 template <int D>
-cudaError_t launch_paged_attn(int dtype, int rot, const PagedAttnArgs& a, int sm_count,
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int max_q_len, int sm_count,
                               cudaStream_t stream) {
   unsigned* st;
   cudaError_t e = detail::paged_status_ptr(&st);
   if (e != cudaSuccess) return e;
-  if (rot == kRotSRFT)
-    return dtype == kDtF16 ? detail::attn_simple<D, kRotSRFT, kDtF16>(a, stream, st)
-                           : detail::attn_simple<D, kRotSRFT, kDtBF16>(a, stream, st);
-  return dtype == kDtF16 ? detail::attn_simple<D, kRotSRHT, kDtF16>(a, stream, st)
-                         : detail::attn_simple<D, kRotSRHT, kDtBF16>(a, stream, st);
+  return few_rows_item(int64_t(max_q_len) * a.n_q) == 8
+             ? detail::few_rows_group<D, 8>(a, sm_count, stream, st)
+             : detail::few_rows_group<D, 16>(a, sm_count, stream, st);
 }
 
 template <int D>

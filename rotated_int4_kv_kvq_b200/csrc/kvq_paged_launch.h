@@ -58,9 +58,21 @@ struct PagedAttnArgs {
   const float *k_scales, *v_scales;
   const int8_t* signs;
   int64_t n_tokens, n_pages, max_pages;
-  int n_seqs, n_kv, n_q, page_shift, group, window;
+  int n_seqs, n_kv, n_q, page_shift, d, group, window, dtype, rot;
   float qscale;  // sm_scale * log2(e)
+  // workspace, cut up by the launcher
+  uint8_t* workspace;
+  struct JoinInfo* join;
+  float* parts;
 };
+
+// Rows of an item of the few-rows kernel for this many rows a sequence and
+// head, and its workspace.
+constexpr int64_t kMaxBlocks = 148 * 4;  // of the few-rows kernel
+constexpr int few_rows_item(int64_t rows) { return rows <= 8 ? 8 : 16; }
+constexpr int64_t few_rows_workspace(int d, int64_t rows) {
+  return kMaxBlocks * 32 + kMaxBlocks * 2 * few_rows_item(rows) * (int64_t(d) + 2) * 4;
+}
 
 // Implemented once per d in the matching translation unit.
 template <int D>
@@ -69,7 +81,7 @@ template <int D>
 cudaError_t launch_append(int dtype, int rot, int group, const AppendArgs& a, int sm_count,
                           cudaStream_t stream);
 template <int D>
-cudaError_t launch_paged_attn(int dtype, int rot, const PagedAttnArgs& a, int sm_count,
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int max_q_len, int sm_count,
                               cudaStream_t stream);
 template <int D>
 cudaError_t read_paged_status(uint32_t* value, bool clear);

@@ -1,0 +1,181 @@
+// kvq_sched.cuh -- how attention over the paged cache is divided among blocks.
+//
+// An item is one tile of up to M query rows (row = token * n_q + query) of a
+// sequence and a KV head; it costs as many units as it has tiles of KT cached
+// rows to attend (one, for rows that attend nothing: their zeros have to be
+// written).  The units of all items, in order of (sequence, head, row tile),
+// are cut into equal runs, one a block, so that ragged lengths and few rows
+// alike load every SM.  An item that several blocks share leaves a partial
+// result of each, and a second kernel joins them.  Lengths live on the device,
+// so each block finds its run itself.
+#pragma once
+
+#include "kvq_rope.cuh"
+
+namespace kvq {
+
+struct SeqInfo {
+  int c0, n, len;  // first token, new tokens, cached rows; n = 0: nothing to do
+};
+
+__device__ __forceinline__ SeqInfo load_seq(const PagedAttnArgs& a, int s, unsigned* status) {
+  const int b = __ldg(a.cu_q + s), e = __ldg(a.cu_q + s + 1), len = __ldg(a.kv_len + s);
+  if (b < 0 || e < b || e > a.n_tokens || len < 0 || len > (a.max_pages << a.page_shift)) {
+    if (status != nullptr) flag_bad_index(status);
+    return SeqInfo{0, 0, 0};
+  }
+  return SeqInfo{b, e - b, len};
+}
+
+// Tiles of cached rows of row tile qt: first tile and their number.
+template <int M, int KT>
+__device__ __forceinline__ void item_tiles(const PagedAttnArgs& a, const SeqInfo& q, int qt,
+                                           int& first, int& count) {
+  const int last_row = min(int64_t(q.n) * a.n_q, (int64_t(qt) + 1) * M) - 1;
+  const int64_t p0 = int64_t(q.len) - q.n + int64_t(qt) * M / a.n_q;
+  const int64_t hi = int64_t(q.len) - q.n + last_row / a.n_q + 1;
+  const int64_t lo = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
+  if (hi <= lo) {
+    first = 0;
+    count = 1;
+  } else {
+    first = int(lo / KT);
+    count = int((hi + KT - 1) / KT) - first;
+  }
+}
+
+template <int M>
+__device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, const SeqInfo& q) {
+  return int((int64_t(q.n) * a.n_q + M - 1) / M);
+}
+
+// Units of one head of a sequence.
+template <int M, int KT>
+__device__ __forceinline__ int64_t head_units(const PagedAttnArgs& a, const SeqInfo& q) {
+  int64_t u = 0;
+  const int nqt = row_tiles<M>(a, q);
+  for (int qt = 0; qt < nqt; ++qt) {
+    int f, c;
+    item_tiles<M, KT>(a, q, qt, f, c);
+    u += c;
+  }
+  return u;
+}
+
+// A place in the order of units.
+template <int M, int KT>
+struct Cursor {
+  SeqInfo q;
+  int seq, head, qt, nqt, first, count, tile;
+
+  __device__ __forceinline__ void item(const PagedAttnArgs& a) {
+    item_tiles<M, KT>(a, q, qt, first, count);
+  }
+  // To the first unit of the next item; the caller knows that there is one.
+  __device__ __forceinline__ void next_item(const PagedAttnArgs& a) {
+    tile = 0;
+    if (++qt == nqt) {
+      qt = 0;
+      if (++head == a.n_kv) {
+        head = 0;
+        do {
+          q = load_seq(a, ++seq, nullptr);
+        } while (q.n == 0 && seq + 1 < a.n_seqs);
+        nqt = row_tiles<M>(a, q);
+      }
+    }
+    item(a);
+  }
+  __device__ __forceinline__ void seek(const PagedAttnArgs& a, int s, int64_t off) {
+    seq = s;
+    q = load_seq(a, s, nullptr);
+    nqt = row_tiles<M>(a, q);
+    const int64_t per_head = head_units<M, KT>(a, q);
+    head = int(off / per_head);
+    off -= head * per_head;
+    for (qt = 0;; ++qt) {
+      item(a);
+      if (off < count) break;
+      off -= count;
+    }
+    tile = int(off);
+  }
+};
+
+struct Run {
+  int64_t total, begin, end;  // units of the call, and of this block
+  int blocks;                 // that have units: the first ones, none in between without
+  int seq;                    // sequence of unit `begin`
+  int64_t off;                // units of that sequence before it
+};
+
+// The run of block b of `blocks`; called by all NT threads, `s` scratch for
+// NT / 32 + 4 values.
+template <int M, int KT, int NT>
+__device__ __forceinline__ Run find_run(const PagedAttnArgs& a, int b, int blocks, int64_t* s,
+                                        unsigned* status) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto scan = [&](int base, int64_t& mine, int64_t& incl) {  // units of seqs base + tid
+    const int sq = base + tid;
+    mine = 0;
+    if (sq < a.n_seqs) {
+      const SeqInfo q = load_seq(a, sq, b == 0 ? status : nullptr);
+      if (q.n > 0) mine = head_units<M, KT>(a, q) * a.n_kv;
+    }
+    incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += up;
+    }
+    __syncthreads();  // the scratch of the call before is read
+    if (lane == 31) s[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    for (int w = 0; w < warp; ++w) before += s[w];
+    incl += before;
+    int64_t all = 0;
+    for (int w = 0; w < NT / 32; ++w) all += s[w];
+    return all;
+  };
+  Run r{0, 0, 0, 0, 0, 0};
+  int64_t mine, incl;
+  for (int base = 0; base < a.n_seqs; base += NT) r.total += scan(base, mine, incl);
+  r.blocks = int(min(int64_t(blocks), r.total));
+  if (b >= r.blocks) return r;
+  r.begin = r.total * b / r.blocks;
+  r.end = r.total * (b + 1) / r.blocks;
+  int64_t before = 0;
+  for (int base = 0; base < a.n_seqs; base += NT) {
+    // one chunk: the scan above still holds
+    const int64_t all = a.n_seqs <= NT ? r.total : scan(base, mine, incl);
+    if (r.begin < before + all) {
+      const int64_t end = before + incl, start = end - mine;
+      if (start <= r.begin && r.begin < end) {
+        s[NT / 32] = base + tid;
+        s[NT / 32 + 1] = r.begin - start;
+      }
+      break;
+    }
+    before += all;
+  }
+  __syncthreads();
+  r.seq = int(s[NT / 32]);
+  r.off = s[NT / 32 + 1];
+  return r;
+}
+
+// The block whose run holds unit u (the inverse of find_run's cuts): the
+// largest b with floor(total b / blocks) <= u.
+__device__ __forceinline__ int block_of(int64_t u, int64_t total, int blocks) {
+  return int(((u + 1) * blocks - 1) / total);
+}
+
+// What the second kernel needs to join an item: written by every block, the
+// item that ends in the block but began in an earlier one.
+struct JoinInfo {
+  int first_block;  // block in which it began (its slot 1), or -1: nothing to join
+  int c0, head, row0, rows;
+};
+
+}  // namespace kvq
