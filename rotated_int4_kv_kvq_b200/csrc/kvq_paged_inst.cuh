@@ -75,27 +75,22 @@ cudaError_t append_group(const AppendArgs& a, int group, int sm_count, cudaStrea
   return cudaErrorInvalidValue;
 }
 
-// Resident blocks per SM of an attention kernel, its shared memory opted into
-// (looked up once per kernel and device).
+// Opts an attention kernel into its shared memory (once per kernel and device).
 template <auto Kern>
-cudaError_t paged_occupancy(int threads, int smem, int* out) {
+cudaError_t paged_setup(int smem) {
   constexpr int kMax = 64;
-  static int occ[kMax];
+  static bool done[kMax];
   static std::mutex mu;
   int dev;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMax) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> g(mu);
-  if (occ[dev] == 0) {
+  if (!done[dev]) {
     e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int b = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, Kern, threads, smem);
-    if (e != cudaSuccess) return e;
-    occ[dev] = std::max(b, 1);
+    done[dev] = true;
   }
-  *out = occ[dev];
   return cudaSuccess;
 }
 
@@ -103,20 +98,18 @@ template <int D, int R, int NG>
 cudaError_t few_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t stream, unsigned* st) {
   using C = Pd<D, R, NG>;
   constexpr auto kern = kvq_paged_decode_kernel<D, R, NG>;
-  int occ;
-  cudaError_t e = paged_occupancy<kern>(kPdThreads, C::SMEM, &occ);
+  cudaError_t e = paged_setup<kern>(C::SMEM);
   if (e != cudaSuccess) return e;
-  // no more blocks than there can be units, or than can be resident at once
-  // (in shared and in tensor memory)
+  // no more blocks than can be resident at once, or than there can be units
   const int64_t items = (args.n_tokens * args.n_q + R - 1) / R + args.n_seqs;
   const int64_t tiles = (args.max_pages << args.page_shift) / C::KT + 1;
-  int64_t grid = std::min<int64_t>(int64_t(sm_count) * std::min(occ, 512 / C::TMEM), kMaxBlocks);
+  int64_t grid = std::min<int64_t>(int64_t(sm_count) * C::BLOCKS, kMaxBlocks);
   if (items * args.n_kv < grid) grid = std::min<int64_t>(grid, items * args.n_kv * std::min<int64_t>(tiles, grid));
   PagedAttnArgs a = args;
   static_assert(sizeof(JoinInfo) <= 32, "workspace");
   a.join = reinterpret_cast<JoinInfo*>(a.workspace);
   a.parts = reinterpret_cast<float*>(a.workspace + kMaxBlocks * 32);
-  e = launch_paged(kern, grid, kPdThreads, C::SMEM, stream, a, st);
+  e = launch_paged(kern, grid, kPdThreads + 32, C::SMEM, stream, a, st);
   if (e != cudaSuccess) return e;
   return a.rot == kRotSRFT
              ? launch_paged(kvq_paged_join_kernel<D, R, kRotSRFT>, grid, 256, 0, stream, a)

@@ -28,9 +28,11 @@
 // accumulated in fp32 after every tile, so it is never rescaled in place.
 //
 // A tile is 128 smem rows of 128 bytes (two tokens a row at d = 64, half a
-// token at d = 256).  One block does, per tile: MMA of the scores while it
-// expands V; softmax; MMA of the values while it expands the next K.  Blocks
-// of one SM (two to four) cover each other's waits.
+// token at d = 256).  Codes travel global -> registers (a tile's time ahead)
+// -> expanded bytes.  Eight warps do, per tile: expand V under the MMA of the
+// scores; softmax; expand the next K under the MMA of the values; accumulate.
+// A ninth warp issues the MMAs and looks the pages up.  The blocks of an SM
+// cover each other's waits.
 #pragma once
 
 #include "kvq_sched.cuh"
@@ -47,6 +49,13 @@ constexpr int pow2_at_least(int x) {
   return p;
 }
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
+constexpr int min_of(int a, int b) { return a < b ? a : b; }
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 template <int D_, int R_, int NG_>
 struct Pd {
@@ -68,27 +77,38 @@ struct Pd {
   static_assert(TMEM <= 512, "tensor memory columns");
   // shared memory
   static constexpr int TILE = NCH * 16384;        // expanded K or V
-  static constexpr int RAW = KT * D / 2;          // packed codes of K or V
-  static constexpr int SC = KT * NG * 4;          // scales of K or V
+  static constexpr int KP = KT * (D / 32) / kPdThreads;  // 16-byte pieces of codes a thread
   static constexpr int QB = NCH * NQS * 128;
   static constexpr int PB = NG * 128 * NP;
   static constexpr int OB = TPR * R * D * 4;      // result of an item, over P
   static constexpr int oK = 0, oV = oK + TILE, oQ = oV + TILE, oP = oQ + QB;
-  static constexpr int oRawK = oP + max_of(PB, OB), oRawV = oRawK + RAW;
-  static constexpr int oSc = oRawV + RAW;         // [2][K, V]
-  static constexpr int oEnd = oSc + 4 * SC;
-  static constexpr int SMEM = oEnd + 1024;        // room to align the base
+  static constexpr int SMEM = oP + max_of(PB, OB) + 1024;  // room to align the base
+  // Blocks an SM: as many as registers, shared and tensor memory hold (the
+  // occupancy calculator answers one for any kernel with tensor memory).
+  static constexpr int BLOCKS = min_of(2, min_of(512 / TMEM, 230000 / (SMEM + 4096)));
+};
+
+// A tile as the control warp writes it down for the others, up to three tiles
+// ahead.
+struct PdTile {
+  int t0, len;          // first token, cached rows of the sequence
+  int c0, head, row0, rows;
+  int p0;               // position of the sequence's first new token
+  int starts, ends;     // first, last tile of its item
+  int pad;
+  int64_t row[16];      // cache row of each 16 tokens, -1: not to be read
 };
 
 struct PdShared {
-  uint64_t kfull, vfull, sdone, odone;
+  uint64_t sdone, odone;
+  PdTile tiles[4];
   uint32_t tmem;
-  uint32_t valid[2];   // 16-token pieces of the tile that lie in the pool
-  int fail;
-  float qs[16], m[16], f[16], icw[16], lsum[16];
+  int fail, began_here;
+  int64_t begun;
+  float qs[16], m[16], f[16], icw[16];
   int pos[16];
   float red[8][16], red2[8][16];
-  int64_t scratch[kPdThreads / 32 + 4];
+  int64_t scratch[kPdThreads / 32 + 1 + 4];
 };
 
 // smem byte of coordinate i (0..D) of a token, before the 128-byte column is
@@ -184,212 +204,262 @@ __device__ __forceinline__ void pd_slices(const uint32_t* w, uint32_t& b0, uint3
 }
 
 template <int D, int R, int NG>
-__global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 ? 3 : 2)
+__global__ void __launch_bounds__(kPdThreads + 32, Pd<D, R, NG>::BLOCKS)
     kvq_paged_decode_kernel(const PagedAttnArgs a, unsigned* status) {
   using C = Pd<D, R, NG>;
-  constexpr int RQ = C::RQ, AQ = C::AQ, KT = C::KT;
+  constexpr int RQ = C::RQ, AQ = C::AQ, KT = C::KT, KP = C::KP;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PdShared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = (warp >> 2) & 1;
   const int row = tid & 127;  // smem row, or coordinate byte, of this thread
-  const uint32_t kfull = smem_u32(&sh.kfull), vfull = smem_u32(&sh.vfull),
-                 sdone = smem_u32(&sh.sdone), odone = smem_u32(&sh.odone);
+  const uint32_t sdone = smem_u32(&sh.sdone), odone = smem_u32(&sh.odone);
   if (tid == 0) {
-    mbar_init(kfull, 1);
-    mbar_init(vfull, 1);
     mbar_init(sdone, 1);
     mbar_init(odone, 1);
     sh.fail = 0;
     fence_mbar_init();
   }
   pdl_wait();  // no global access before the previous kernel completes
-  const Run run = find_run<R, KT, kPdThreads>(a, blockIdx.x, gridDim.x, sh.scratch, status);
+  const Run run = find_run<R, KT, kPdThreads + 32>(a, blockIdx.x, gridDim.x, sh.scratch, status);
   JoinInfo* join = a.join + blockIdx.x;
   if (run.begin == run.end) {
     if (tid == 0) join->first_block = -1;
     return;
   }
-  if (warp == 0) tmem_alloc(smem_u32(&sh.tmem), C::TMEM);
-  Cursor<R, KT> cur;
-  cur.seek(a, run.seq, run.off);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
-  const uint32_t tlane = tmem + (uint32_t(warp & 3) << 21);
+  const int n_tiles = int(run.end - run.begin);
 
-  // ---- loads (warp 7): runs of rows of one page, a lane each ----
-  auto load = [&](const Cursor<R, KT>& c, int buf, bool values) {
-    const int rt = min(1 << a.page_shift, KT);  // tokens of a run
-    const int64_t t0 = int64_t(c.tile + c.first) * KT + lane * rt;
-    int rows = 0;
-    int64_t at = 0;
-    if (lane * rt < KT && t0 < c.q.len) {
-      const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t0 >> a.page_shift));
-      if (page < 0 || page >= a.n_pages) {
-        if (!values) flag_bad_index(status);
-      } else {
-        rows = int(min(int64_t(rt), (c.q.len - t0 + 15) & ~int64_t(15)));
-        at = ((page * a.n_kv + c.head) << a.page_shift) + (t0 & ((1 << a.page_shift) - 1));
-      }
+  if (warp == kPdThreads / 32) {
+    // ================= control: tile descriptions and MMA issue =================
+    tmem_alloc(smem_u32(&sh.tmem), C::TMEM);
+    Cursor<R, KT> c;
+    c.seek(a, run.seq, run.off);
+    if (lane == 0) {
+      join->first_block = -1;
+      sh.begun = run.begin - c.tile;  // unit at which the first item begins
+      sh.began_here = c.tile == 0;
     }
-    const int total = __reduce_add_sync(kFull, rows);
-    const uint32_t bar = values ? vfull : kfull;
-    if (!values) {
-      const uint32_t ok = rows > 0 ? ((1u << (rt / 16)) - 1u) << (lane * (rt / 16)) : 0u;
-      const uint32_t all = __reduce_or_sync(kFull, ok);
-      if (lane == 0) sh.valid[buf] = all;
-    }
-    if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(total) * (D / 2 + (values ? 0 : 8 * NG)));
-    __syncwarp();
-    if (rows > 0) {
-      const uint32_t o = uint32_t(lane * rt);
-      if (values) {
-        bulk_load(sbase + C::oRawV + o * (D / 2), a.v_packed + at * (D / 2), rows * (D / 2), bar);
-      } else {
-        const uint32_t sc = sbase + C::oSc + buf * 2 * C::SC + o * (NG * 4);
-        bulk_load(sbase + C::oRawK + o * (D / 2), a.k_packed + at * (D / 2), rows * (D / 2), bar);
-        bulk_load(sc, a.k_scales + at * NG, rows * NG * 4, bar);
-        bulk_load(sc + C::SC, a.v_scales + at * NG, rows * NG * 4, bar);
+    auto describe = [&](int i) {  // the cursor's tile as number i
+      PdTile& e = sh.tiles[i & 3];
+      const int t0 = (c.first + c.tile) * KT;
+      if (lane == 0) {
+        e.t0 = t0;
+        e.len = c.q.len;
+        e.c0 = c.q.c0;
+        e.head = c.head;
+        e.row0 = c.qt * R;
+        e.rows = int(min(int64_t(R), int64_t(c.q.n) * a.n_q - int64_t(c.qt) * R));
+        e.p0 = c.q.len - c.q.n;
+        e.starts = c.tile == 0;
+        e.ends = c.tile + 1 == c.count;
       }
+      if (lane < KT / 16) {
+        const int64_t t = int64_t(t0) + lane * 16;
+        int64_t r = -1;
+        if (t < c.q.len) {
+          const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
+          if (page < 0 || page >= a.n_pages)
+            flag_bad_index(status);
+          else
+            r = ((page * a.n_kv + c.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+        }
+        e.row[lane] = r;
+      }
+      if (i + 1 < n_tiles && ++c.tile == c.count) c.next_item(a);
+    };
+    for (int i = 0; i < min(3, n_tiles); ++i) describe(i);
+    tc_fence_before();
+    __syncthreads();  // descriptions, tensor memory
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    for (int i = 0; i < n_tiles; ++i) {
+      __syncthreads();  // A
+      if (lane == 0) {
+        tc_fence_after();
+        constexpr uint32_t id = instr_desc(kAccS32, kFmtS8, kFmtS8, false, false, 128, C::NQS);
+#pragma unroll
+        for (int b = 0; b < C::SBLK; ++b) {
+          const int half = b / NG, j = b % NG;
+#pragma unroll
+          for (int k = 0; k < C::G; k += 32) {
+            const int byte = j * C::G + k;  // in the token's bytes
+            const int abyte = C::TPR == 2 ? half * 64 + byte : byte;
+            mma_i8(tmem + b * C::NQS,
+                   smem_desc(sbase + C::oK + (abyte >> 7) * 16384 + (abyte & 127), 16, 1024, kSw128),
+                   smem_desc(sbase + C::oQ + (byte >> 7) * (C::NQS * 128) + (byte & 127), 16, 1024,
+                             kSw128),
+                   id, k > 0);
+          }
+        }
+        mma_commit(sdone);
+      }
+      __syncwarp();
+      const bool ends = sh.tiles[i & 3].ends || i + 1 == n_tiles;
+      if (i + 3 < n_tiles) describe(i + 3);
+      if (__syncthreads_or(0)) {  // B
+        if (sh.fail) break;
+        __syncthreads();
+        __syncthreads();
+        __syncthreads();
+      }
+      if (lane == 0) {
+        tc_fence_after();
+        // one MMA for all groups of a 128-coordinate block
+        constexpr uint32_t id =
+            instr_desc(kAccS32, kFmtS8, kFmtU8, true, true, 128, C::NGM * C::NP);
+#pragma unroll
+        for (int mt = 0; mt < C::NCH; ++mt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_i8(tmem + mt * C::NGM * C::NP,
+                   smem_desc(sbase + C::oV + mt * 16384 + k * 4096, 16, 1024, kSw128),
+                   smem_desc(sbase + C::oP + (NG == 1 ? 0 : mt * C::NGM * 128 * C::NP) +
+                                 k * 32 * C::NP,
+                             128 * C::NP, 8 * C::NP, C::PSW),
+                   id, k > 0);
+        mma_commit(odone);
+      }
+      __syncwarp();
+      if (ends) __syncthreads();  // results of the item
+    }
+    __syncthreads();  // every read of tensor memory is done
+    tmem_free(tmem, C::TMEM);
+    return;
+  }
+
+  // ========================== the eight other warps ==========================
+  __syncthreads();  // descriptions, tensor memory
+  tc_fence_after();
+  const uint32_t tlane = sh.tmem + (uint32_t(warp & 3) << 21);
+  const int tl = C::TPR == 2 ? wg * 128 + row : row;  // token of this thread's scores
+  const int q0 = C::TPR == 2 ? 0 : wg * RQ;           // its first query row
+  const int half = C::TPR == 2 ? row >> 6 : 0;        // of the accumulators: d = 64 half,
+  const int crd = C::TPR == 2 ? row & 63 : row;       // coordinate byte,
+  const int a0 = D == 256 ? 0 : wg * AQ;              // first query row
+
+  // Packed codes of a tile in registers: piece tid + 256 k of 16 bytes, each
+  // loaded a tile's time before it is expanded.
+  uint4 kreg[KP], vreg[KP];
+  float ks[NG], vs[NG];
+  bool seen;
+  auto load_codes = [&](int i, const uint8_t* base, uint4 (&w)[KP]) {
+    const PdTile& e = sh.tiles[i & 3];
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+      const int p = tid + kPdThreads * k, t = p / (D / 32);
+      const int64_t r = e.row[t >> 4];
+      w[k] = make_uint4(0, 0, 0, 0);
+      if (r >= 0)
+        w[k] = __ldg(reinterpret_cast<const uint4*>(base + (r + (t & 15)) * (D / 2)) + p % (D / 32));
     }
   };
-  // ---- packed codes -> 16 c bytes in a swizzled tile ----
-  auto expand = [&](uint32_t raw, uint32_t tile) {
-    constexpr int PIECES = KT * (D / 32);  // of 16 bytes, 32 codes
-#pragma unroll 4
-    for (int i = tid; i < PIECES; i += kPdThreads) {
-      const uint4 w = lds128(raw + uint32_t(i) * 16);
-      const int t = i / (D / 32), p = i % (D / 32);
+  auto load_scales = [&](int i) {
+    const PdTile& e = sh.tiles[i & 3];
+    const int64_t r = e.row[tl >> 4];
+    seen = r >= 0 && e.t0 + tl < e.len;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) ks[j] = vs[j] = 0.0f;
+    if (seen) {
+      const float* kp = a.k_scales + (r + (tl & 15)) * NG;
+      const float* vp = a.v_scales + (r + (tl & 15)) * NG;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) ks[j] = __ldg(kp + j), vs[j] = __ldg(vp + j);
+    }
+  };
+  // -> 16 c bytes in a swizzled tile
+  auto expand = [&](const uint4 (&w)[KP], uint32_t tile) {
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+      const int p = tid + kPdThreads * k, t = p / (D / 32);
       const int r = t & 127;
-      const int byte = (t >> 7) * 64 + p * 32;  // in the token's bytes (d = 64: by half)
+      const int byte = (t >> 7) * 64 + p % (D / 32) * 32;  // in the row's bytes
       const uint32_t base = tile + uint32_t(byte >> 7) * 16384 + uint32_t(r) * 128;
       const uint32_t c0 = (uint32_t(byte & 127) >> 4) ^ uint32_t(r & 7), c1 = c0 ^ 1u;
       constexpr uint32_t H = 0xF0F0F0F0u;
-      sts128(base + c0 * 16, (w.x << 4) & H, w.x & H, (w.y << 4) & H, w.y & H);
-      sts128(base + c1 * 16, (w.z << 4) & H, w.z & H, (w.w << 4) & H, w.w & H);
+      sts128(base + c0 * 16, (w[k].x << 4) & H, w[k].x & H, (w[k].y << 4) & H, w[k].y & H);
+      sts128(base + c1 * 16, (w[k].z << 4) & H, w[k].z & H, (w[k].w << 4) & H, w[k].w & H);
     }
-    fence_proxy_async_smem();
   };
 
-  // ---- per-item state ----
-  int n_rows = 0, row0 = 0;
   float m[RQ], l[RQ], cw[RQ], acc[AQ];
   bool fresh = true;
-  auto start_item = [&]() {
-    row0 = cur.qt * R;
-    n_rows = int(min(int64_t(R), int64_t(cur.q.n) * a.n_q - row0));
+  auto start_item = [&](const PdTile& e) {
 #pragma unroll
     for (int r = 0; r < RQ; ++r) m[r] = -3e38f, l[r] = 0.0f, cw[r] = 1.0f;
 #pragma unroll
     for (int r = 0; r < AQ; ++r) acc[r] = 0.0f;
     fresh = true;
-    for (int r = warp; r < n_rows; r += kPdThreads / 32) {
-      const int tok = (row0 + r) / a.n_q;
-      const uint16_t* src = a.q + (int64_t(cur.q.c0) + tok) * a.q_stride +
-                            (int64_t(cur.head) * a.n_q + (row0 + r - tok * a.n_q)) * D;
+    for (int r = warp; r < e.rows; r += kPdThreads / 32) {
+      const int tok = (e.row0 + r) / a.n_q;
+      const uint16_t* src = a.q + (int64_t(e.c0) + tok) * a.q_stride +
+                            (int64_t(e.head) * a.n_q + (e.row0 + r - tok * a.n_q)) * D;
       const float qs = a.rot == kRotSRFT ? pd_query<C, kRotSRFT>(a, src, smem + C::oQ, r, lane)
                                          : pd_query<C, kRotSRHT>(a, src, smem + C::oQ, r, lane);
       if (lane == 0) {
         sh.qs[r] = qs;
-        sh.pos[r] = cur.q.len - cur.q.n + tok;
+        sh.pos[r] = e.p0 + tok;
         sh.m[r] = -3e38f;
       }
     }
-    fence_proxy_async_smem();
   };
 
-  Cursor<R, KT> ahead = cur;  // warp 7: the tile whose loads were issued last
-  if (warp == 7) {
-    load(ahead, 0, false);
-    load(ahead, 0, true);
-  }
-  start_item();
-  bool ok = mbar_wait_bounded(kfull, 0);
-  expand(sbase + C::oRawK, sbase + C::oK);
+  load_codes(0, a.k_packed, kreg);
+  load_codes(0, a.v_packed, vreg);
+  load_scales(0);
+  start_item(sh.tiles[0]);
+  expand(kreg, sbase + C::oK);
+  if (n_tiles > 1) load_codes(1, a.k_packed, kreg);
+  fence_proxy_async_smem();
+  bool began_here = sh.began_here, ok = true;
 
-  bool began_here = cur.tile == 0;
-  if (tid == 0) join->first_block = -1;
-  const int64_t item_begin = run.begin - cur.tile;  // unit of the first item's first tile
-  for (int64_t u = run.begin; u < run.end; ++u) {
-    const uint32_t par = uint32_t(u - run.begin) & 1u;
-    const int buf = int(par);
-    const bool more = u + 1 < run.end;
+  for (int i = 0; i < n_tiles; ++i) {
+    const PdTile& e = sh.tiles[i & 3];
+    const uint32_t par = uint32_t(i) & 1u;
+    const bool more = i + 1 < n_tiles;
     __syncthreads();  // A: K and the queries are in shared memory, O is read
-    if (tid == 0) {
-      tc_fence_after();
-      constexpr uint32_t id =
-          instr_desc(kAccS32, kFmtS8, kFmtS8, false, false, 128, C::NQS);
-#pragma unroll
-      for (int b = 0; b < C::SBLK; ++b) {
-        const int half = b / NG, j = b % NG;
-#pragma unroll
-        for (int k = 0; k < C::G; k += 32) {
-          const int byte = j * C::G + k;  // in the token's bytes
-          const int abyte = C::TPR == 2 ? half * 64 + byte : byte;
-          mma_i8(tmem + b * C::NQS,
-                 smem_desc(sbase + C::oK + (abyte >> 7) * 16384 + (abyte & 127), 16, 1024, kSw128),
-                 smem_desc(sbase + C::oQ + (byte >> 7) * (C::NQS * 128) + (byte & 127), 16, 1024,
-                           kSw128),
-                 id, k > 0);
-        }
-      }
-      mma_commit(sdone);
-    }
-    if (warp == 7 && more) {
-      if (++ahead.tile == ahead.count) ahead.next_item(a);
-      load(ahead, buf ^ 1, false);
-    }
-    ok = mbar_wait_bounded(vfull, par) && ok;
-    expand(sbase + C::oRawV, sbase + C::oV);
+    expand(vreg, sbase + C::oV);
+    if (more) load_codes(i + 1, a.v_packed, vreg);
 
     // ---- scores of this thread's token ----
+    const int nr = min(max(e.rows - q0, 0), RQ);
+    const int t = e.t0 + tl;
+    const int pf = e.p0 + e.row0 / a.n_q;  // positions of the first and the last row
+    const int pl = e.p0 + (e.row0 + e.rows - 1) / a.n_q;
+    const bool whole = e.t0 + KT - 1 <= pf && (a.window == 0 || e.t0 > pl - a.window);
+    const float vmax = [&] {
+      float x = vs[0];
+#pragma unroll
+      for (int j = 1; j < NG; ++j) x = fmaxf(x, vs[j]);
+      return x;
+    }();
     ok = mbar_wait_bounded(sdone, par) && ok;
     tc_fence_after();
-    const int tl = C::TPR == 2 ? wg * 128 + row : row;
-    const int64_t t0 = int64_t(cur.first + cur.tile) * KT, t = t0 + tl;
-    const int q0 = C::TPR == 2 ? 0 : wg * RQ;   // first query row of this thread
-    const int nr = min(max(n_rows - q0, 0), RQ);
-    const float* ksc = reinterpret_cast<const float*>(smem + C::oSc + buf * 2 * C::SC) + tl * NG;
-    const float* vsc = ksc + C::SC / 4;
-    const int pf = cur.q.len - cur.q.n + row0 / a.n_q;  // positions of the first and last row
-    const int pl = cur.q.len - cur.q.n + (row0 + n_rows - 1) / a.n_q;
-    const bool whole = t0 + KT - 1 <= pf && (a.window == 0 || t0 > int64_t(pl) - a.window) &&
-                       sh.valid[buf] == (1u << (KT / 16)) - 1u;
-    float s[RQ], vs[NG], vmax;
-    bool seen = true;
-    if (!whole) seen = ((sh.valid[buf] >> (tl / 16)) & 1u) && t < cur.q.len;
+    float s[RQ];
+    {
+      uint32_t x[NG][2 * RQ];
 #pragma unroll
-    for (int r = 0; r < RQ; ++r) s[r] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      uint32_t x[2 * RQ];
-      tmem_ld<2 * RQ>(tlane + uint32_t(((C::TPR == 2 ? wg * NG : 0) + j) * C::NQS + q0 * 2), x);
-      const float k = ksc[j];
-      vs[j] = seen ? vsc[j] : 0.0f;
+      for (int j = 0; j < NG; ++j)
+        tmem_ld<2 * RQ>(tlane + uint32_t(((C::TPR == 2 ? wg * NG : 0) + j) * C::NQS + q0 * 2), x[j]);
       tmem_wait_ld();
 #pragma unroll
       for (int r = 0; r < RQ; ++r)
-        if (r < nr) s[r] = fmaf(k, float(int(x[r]) * 128 + int(x[RQ + r])), s[r]);
-    }
-    vmax = vs[0];
+        if (r < nr) {
+          float v = 0.0f;
 #pragma unroll
-    for (int j = 1; j < NG; ++j) vmax = fmaxf(vmax, vs[j]);
-#pragma unroll
-    for (int r = 0; r < RQ; ++r)
-      if (r < nr) {
-        s[r] *= sh.qs[q0 + r];
-        if (!whole) {
-          const int p = sh.pos[q0 + r];
-          if (!seen || t > p || (a.window > 0 && t <= int64_t(p) - a.window)) s[r] = -INFINITY;
+          for (int j = 0; j < NG; ++j)
+            v = fmaf(ks[j], float(int(x[j][r]) * 128 + int(x[j][RQ + r])), v);
+          s[r] = v * sh.qs[q0 + r];
+          if (!seen) s[r] = -INFINITY;
+          if (!whole) {
+            const int p = sh.pos[q0 + r];
+            if (t > p || (a.window > 0 && t <= p - a.window)) s[r] = -INFINITY;
+          }
         }
-      }
+    }
 
     // ---- weights and their slices ----
-    uint8_t* prow = smem + C::oP;
     auto weights = [&]() {
       bool over = false;
       float p[RQ];
@@ -398,7 +468,7 @@ __global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 
         p[r] = 0.0f;
         if (r < nr) {
           const float x = s[r] - m[r];
-          p[r] = exp2f(x);
+          p[r] = ex2(x);
           l[r] += p[r];
           over = over || x > 7.0f || p[r] * vmax * cw[r] > 127.0f;
         }
@@ -409,27 +479,28 @@ __global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 
 #pragma unroll
         for (int r = 0; r < RQ; ++r)
           w[r] = __float_as_uint(fmaf(p[r] * vs[j], cw[r] * 65536.0f, 8388608.0f));
-        uint32_t b[3 * RQ / 4];
+        constexpr int NB = 3 * RQ / 4;
+        uint32_t b[(NB + 3) / 4 * 4];
+#pragma unroll
+        for (int r = NB; r < (NB + 3) / 4 * 4; ++r) b[r] = 0u;
 #pragma unroll
         for (int r = 0; r < RQ / 4; ++r)
           pd_slices(w + 4 * r, b[r], b[RQ / 4 + r], b[RQ / 2 + r]);
         // row of 2 PW bytes, this thread's half of it; 16-byte pieces swizzled
-        const uint32_t base = smem_u32(prow) + uint32_t(j * 128 + row) * C::NP;
+        const uint32_t base = sbase + C::oP + uint32_t(j * 128 + row) * C::NP;
         const uint32_t x = C::NP == 32 ? (row >> 2) & 1 : (C::NP == 64 ? (row >> 1) & 3 : row & 7);
 #pragma unroll
-        for (int i = 0; i < 3 * RQ / 4; i += 4)
-          sts128(base + ((uint32_t(wg * (C::PW / 16) + i / 4) ^ x) * 16), b[i],
-                 i + 1 < 3 * RQ / 4 ? b[i + 1 < 3 * RQ / 4 ? i + 1 : 0] : 0u,
-                 i + 2 < 3 * RQ / 4 ? b[i + 2 < 3 * RQ / 4 ? i + 2 : 0] : 0u,
-                 i + 3 < 3 * RQ / 4 ? b[i + 3 < 3 * RQ / 4 ? i + 3 : 0] : 0u);
+        for (int k = 0; k < NB; k += 4)
+          sts128(base + ((uint32_t(wg * (C::PW / 16) + k / 4) ^ x) * 16), b[k], b[k + 1], b[k + 2],
+                 b[k + 3]);
       }
-      fence_proxy_async_smem();
+      fence_proxy_async_smem();  // V's stores too
       return over;
     };
     float lold[RQ];
 #pragma unroll
     for (int r = 0; r < RQ; ++r) lold[r] = l[r];
-    bool over = fresh ? true : weights();
+    const bool over = fresh ? true : weights();
     if (!ok) sh.fail = 1;
     tc_fence_before();
     const bool slow = __syncthreads_or(over || !ok);  // B: V and P are in shared memory
@@ -454,10 +525,10 @@ __global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 
 #pragma unroll
           for (int w = 0; w < 4; ++w) mn = fmaxf(mn, sh.red[(wg ^ 1) * 4 + w][r]);
         }
-        const float f = exp2f(m[r] - mn);
+        const float f = ex2(m[r] - mn);
         l[r] *= f;
         m[r] = mn;
-        float x = r < nr ? exp2f(s[r] - mn) * vmax : 0.0f;
+        float x = r < nr ? ex2(s[r] - mn) * vmax : 0.0f;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
         if (lane == 0) sh.red2[warp][r] = x;
@@ -477,47 +548,28 @@ __global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 
           for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.red2[(wg ^ 1) * 4 + w][r]);
         }
         // the power of two that brings the largest into [1/2, 1)
-        const int e = min(max(253 - int(__float_as_uint(x) >> 23), 1), 237);
-        cw[r] = __uint_as_float(uint32_t(e) << 23);
+        const int ex = min(max(253 - int(__float_as_uint(x) >> 23), 1), 237);
+        cw[r] = __uint_as_float(uint32_t(ex) << 23);
         if (row == 0 && (C::TPR == 1 || wg == 0))
-          sh.icw[q0 + r] = __uint_as_float(uint32_t(254 - e) << 23);
+          sh.icw[q0 + r] = __uint_as_float(uint32_t(254 - ex) << 23);
       }
       weights();
       __syncthreads();
     }
     fresh = false;
-    if (tid == 0) {
-      tc_fence_after();
-      constexpr uint32_t id = instr_desc(kAccS32, kFmtS8, kFmtU8, true, true, 128, C::NP);
-#pragma unroll
-      for (int b = 0; b < C::NCH * C::NGM; ++b) {
-        const int mt = b / C::NGM, j = NG == 1 ? 0 : b;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_i8(tmem + b * C::NP,
-                 smem_desc(sbase + C::oV + mt * 16384 + k * 4096, 16, 1024, kSw128),
-                 smem_desc(sbase + C::oP + j * 128 * C::NP + k * 32 * C::NP, 16, 8 * C::NP, C::PSW),
-                 id, k > 0);
-      }
-      mma_commit(odone);
-    }
     if (more) {
-      if (warp == 7) load(ahead, buf ^ 1, true);
-      ok = mbar_wait_bounded(kfull, par ^ 1u) && ok;
-      expand(sbase + C::oRawK, sbase + C::oK);
+      load_scales(i + 1);
+      expand(kreg, sbase + C::oK);
+      if (i + 2 < n_tiles) load_codes(i + 2, a.k_packed, kreg);
     }
 
     // ---- accumulate the tile's O: this thread's coordinate, its query rows ----
     ok = mbar_wait_bounded(odone, par) && ok;
     tc_fence_after();
-    const int half = C::TPR == 2 ? row >> 6 : 0;          // d = 64: tokens of the byte's half
-    const int crd = C::TPR == 2 ? row & 63 : row;
-    const int blk = D == 256 ? wg * C::NGM + crd / max_of(C::G > 128 ? 128 : C::G, 1)
-                             : crd / C::G;
-    const int a0 = D == 256 ? 0 : wg * AQ;                // first query row
     // The columns of a query row: segment of P (the byte's half at d = 64, wg at
     // d = 128, both in turn at d = 256), slice, row in the segment.
     constexpr int HN = D == 256 ? 2 : 1, CN = AQ / HN;
+    const int blk = D == 256 ? wg * C::NGM + crd / (C::G > 128 ? 128 : C::G) : crd / C::G;
 #pragma unroll
     for (int h = 0; h < HN; ++h) {
       const int seg = D == 64 ? half : (D == 128 ? wg : h);
@@ -529,10 +581,10 @@ __global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 
       tmem_ld<CN>(at + 2 * RQ, x2);
       tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < CN; ++i) {
-        const int ai = h * CN + i, r = a0 + ai;
-        if (r < n_rows) {
-          const float v = fmaf(float(int(x2[i])), 65536.0f, float(int(x1[i]) * 256 + int(x0[i])));
+      for (int k = 0; k < CN; ++k) {
+        const int ai = h * CN + k, r = a0 + ai;
+        if (r < e.rows) {
+          const float v = fmaf(float(int(x2[k])), 65536.0f, float(int(x1[k]) * 256 + int(x0[k])));
           if (slow) acc[ai] *= sh.f[r];
           acc[ai] = fmaf(v, sh.icw[r] * (1.0f / 1048576.0f), acc[ai]);
         }
@@ -541,8 +593,7 @@ __global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 
     tc_fence_before();
 
     // ---- end of the item, or of the block's share of it ----
-    const bool ends = cur.tile + 1 == cur.count;
-    if (ends || !more) {
+    if (e.ends || !more) {
 #pragma unroll
       for (int r = 0; r < RQ; ++r) {
         float x = l[r];
@@ -550,13 +601,13 @@ __global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 
         for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
         if (lane == 0) sh.red[warp][r] = x;
       }
-      const bool whole_item = ends && began_here;
+      const bool complete = e.ends && began_here;
       const int dim = D == 256 ? wg * 128 + pd_dim(row) : pd_dim(crd);
       float* ob = reinterpret_cast<float*>(smem + C::oP);
 #pragma unroll
-      for (int i = 0; i < AQ; ++i) ob[(half * R + a0 + i) * D + dim] = acc[i];
+      for (int k = 0; k < AQ; ++k) ob[(half * R + a0 + k) * D + dim] = acc[k];
       __syncthreads();
-      for (int r = warp; r < n_rows; r += kPdThreads / 32) {
+      for (int r = warp; r < e.rows; r += kPdThreads / 32) {
         float ls = 0.0f;
         const int w0 = C::TPR == 2 ? 0 : (r / RQ) * 4;
         for (int w = 0; w < (C::TPR == 2 ? 8 : 4); ++w) ls += sh.red[w0 + w][r % RQ];
@@ -565,9 +616,9 @@ __global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 
           if constexpr (C::TPR == 2) v += ob[(R + r) * D + d];
           return v;
         };
-        if (whole_item) {
+        if (complete) {
           const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
-          uint16_t* dst = out_row(a, cur.q.c0, cur.head, row0 + r);
+          uint16_t* dst = out_row(a, e.c0, e.head, e.row0 + r);
           float Y[D / 32];
           if (a.rot == kRotSRFT) {
             WideLane<D, kRotSRFT> L;
@@ -590,32 +641,23 @@ __global__ void __launch_bounds__(kPdThreads, D <= 128 && Pd<D, R, NG>::RQ == 4 
           for (int d = lane; d < D; d += 32) slot[2 * R + r * D + d] = value(d);
         }
       }
-      if (ends && !began_here && tid == 0) {
-        join->c0 = cur.q.c0;
-        join->head = cur.head;
-        join->row0 = row0;
-        join->rows = n_rows;
-        join->first_block = block_of(item_begin, run.total, run.blocks);
+      if (e.ends && !began_here && tid == 0) {
+        join->c0 = e.c0;
+        join->head = e.head;
+        join->row0 = e.row0;
+        join->rows = e.rows;
+        join->first_block = block_of(sh.begun, run.total, run.blocks);
       }
-      if (ends && more) {
-        cur.next_item(a);
+      if (more) {
         began_here = true;
-        start_item();
+        start_item(sh.tiles[(i + 1) & 3]);
       }
-    } else {
-      ++cur.tile;
     }
+    fence_proxy_async_smem();  // K's and the queries' stores
   }
-  if (!ok) {  // give the copies in flight a (bounded) chance to land
-    atomicOr(status, kPagedTimeout);
-    for (uint32_t p = 0; p < 2; ++p) {
-      mbar_wait_bounded(kfull, p);
-      mbar_wait_bounded(vfull, p);
-    }
-  }
+  if (!ok) atomicOr(status, kPagedTimeout);
   pdl_release();
-  __syncthreads();
-  if (warp == 0) tmem_free(tmem, C::TMEM);
+  __syncthreads();  // every read of tensor memory is done
 }
 
 // Joins the partial results of items that several blocks shared: block b the
