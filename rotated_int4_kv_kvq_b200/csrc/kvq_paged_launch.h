@@ -66,12 +66,15 @@ struct PagedAttnArgs {
   float* parts;
 };
 
-// Rows of an item of the few-rows kernel for this many rows a sequence and
-// head, and its workspace.
+// Rows of an item of the few-rows kernel for this many rows of a sequence and
+// KV head: fewer columns cost less of everything, and 16 do not fit shared
+// and tensor memory with 4 or 8 groups of a 256-value row.
+constexpr int few_rows_item(int d, int group, int64_t rows) {
+  return d == 64 && rows <= 4 ? 4 : (rows <= 8 || (d == 256 && group <= 64) ? 8 : 16);
+}
 constexpr int64_t kMaxBlocks = 148 * 4;  // of the few-rows kernel
-constexpr int few_rows_item(int64_t rows) { return rows <= 8 ? 8 : 16; }
-constexpr int64_t few_rows_workspace(int d, int64_t rows) {
-  return kMaxBlocks * 32 + kMaxBlocks * 2 * few_rows_item(rows) * (int64_t(d) + 2) * 4;
+constexpr int64_t few_rows_workspace(int d) {
+  return kMaxBlocks * 32 + kMaxBlocks * 2 * 16 * (int64_t(d) + 2) * 4;
 }
 
 // Implemented once per d in the matching translation unit.

@@ -28,11 +28,11 @@
 // accumulated in fp32 after every tile, so it is never rescaled in place.
 //
 // A tile is 128 smem rows of 128 bytes (two tokens a row at d = 64, half a
-// token at d = 256).  Codes travel global -> registers (a tile's time ahead)
-// -> expanded bytes.  Eight warps do, per tile: expand V under the MMA of the
-// scores; softmax; expand the next K under the MMA of the values; accumulate.
-// A ninth warp issues the MMAs and looks the pages up.  The blocks of an SM
-// cover each other's waits.
+// token at d = 256).  A block is a pipeline of roles: four warps expand codes
+// (global -> registers a tile ahead -> bytes), four turn scores into weights,
+// four accumulate results and prepare the queries of the next item, one looks
+// pages up, prefetches into L2 and issues the MMAs.  Operands, scores and
+// results are double-buffered, so the roles work on neighbouring tiles at once.
 #pragma once
 
 #include "kvq_sched.cuh"
@@ -41,7 +41,7 @@
 
 namespace kvq {
 
-constexpr int kPdThreads = 256;
+constexpr int kPdThreads = 13 * 32;
 
 constexpr int pow2_at_least(int x) {
   int p = 32;
@@ -64,51 +64,57 @@ struct Pd {
   static constexpr int NCH = D == 256 ? 2 : 1;    // 128-byte columns of a token
   static constexpr int TPR = D == 64 ? 2 : 1;     // tokens of an smem row
   static constexpr int KT = 128 * TPR;            // tokens of a tile
-  static constexpr int RQ = D == 64 ? R : R / 2;  // query rows of a thread's scores
-  static constexpr int AQ = D == 256 ? R : R / 2;  // query rows of a thread's accumulators
   static constexpr int NQS = 2 * R;               // N of the score MMA
   static constexpr int SBLK = TPR * NG;           // its column blocks
-  // bytes of P a thread writes for its token (3 RQ, to a swizzle width)
-  static constexpr int PW = RQ == 4 ? 16 : (RQ == 8 ? 32 : 64);
-  static constexpr int NP = 2 * PW;               // N of the value MMA
+  // bytes of P of a token and group (3 R, to a swizzle width)
+  static constexpr int PW = R <= 4 ? 16 : (R <= 8 ? 32 : 64);
+  static constexpr int NP = TPR * PW;             // N of the value MMA, for a group
   static constexpr int NGM = D == 256 ? max_of(1, NG / 2) : NG;  // P's of a 128-coordinate block
   static constexpr uint32_t PSW = NP == 32 ? kSw32 : (NP == 64 ? kSw64 : kSw128);
-  static constexpr int TMEM = pow2_at_least(max_of(SBLK * NQS, NCH * NGM * NP));
+  static constexpr int SCOLS = SBLK * NQS, OCOLS = NCH * NGM * NP;
+  static constexpr int OBUF = 2 * SCOLS + 2 * OCOLS <= 256 ? 2 : 1;  // two blocks an SM
+  static constexpr int TMEM = pow2_at_least(2 * SCOLS + OBUF * OCOLS);
   static_assert(TMEM <= 512, "tensor memory columns");
-  // shared memory
+  // shared memory, two of each
   static constexpr int TILE = NCH * 16384;        // expanded K or V
-  static constexpr int KP = KT * (D / 32) / kPdThreads;  // 16-byte pieces of codes a thread
   static constexpr int QB = NCH * NQS * 128;
   static constexpr int PB = NG * 128 * NP;
-  static constexpr int OB = TPR * R * D * 4;      // result of an item, over P
-  static constexpr int oK = 0, oV = oK + TILE, oQ = oV + TILE, oP = oQ + QB;
-  static constexpr int SMEM = oP + max_of(PB, OB) + 1024;  // room to align the base
+  static constexpr int OB = TPR * R * D * 4;      // result of an item (one)
+  static constexpr int oK = 0, oV = 2 * TILE, oQ = 4 * TILE, oP = oQ + 2 * QB, oO = oP + 2 * PB;
+  static constexpr int SMEM = oO + OB + 1024;     // room to align the base
+  static constexpr int KP = KT * (D / 32) / 128;  // 16-byte pieces of codes a thread
   // Blocks an SM: as many as registers, shared and tensor memory hold (the
   // occupancy calculator answers one for any kernel with tensor memory).
-  static constexpr int BLOCKS = min_of(2, min_of(512 / TMEM, 230000 / (SMEM + 4096)));
+  static constexpr int BLOCKS = R > 8 ? 1 : min_of(2, min_of(512 / TMEM, 230000 / (SMEM + 6144)));
+  static_assert(SMEM + 6144 <= 232448, "shared memory");
+  static_assert(R % 4 == 0 && R <= 16 && NP >= 32, "rows");
 };
 
-// A tile as the control warp writes it down for the others, up to three tiles
+// A tile as the control warp writes it down for the others, up to six tiles
 // ahead.
 struct PdTile {
   int t0, len;          // first token, cached rows of the sequence
   int c0, head, row0, rows;
-  int p0;               // position of the sequence's first new token
-  int starts, ends;     // first, last tile of its item
-  int pad;
+  int starts, ends;     // first, last tile of its item (or of the block's share)
+  int whole, last;      // no row's limits lie inside; the item's last tile
   int64_t row[16];      // cache row of each 16 tokens, -1: not to be read
 };
+constexpr int kPdRing = 16;
 
 struct PdShared {
-  uint64_t sdone, odone;
-  PdTile tiles[4];
+  uint64_t dfull[kPdRing];                   // tile described
+  uint64_t kfull[2], vfull[2], pfull[2], qfull[2];  // operands in shared memory
+  uint64_t sdone[2], odone[2];               // MMAs done: S, or O, ready; operands free
+  uint64_t sfree[2], ofree[2];               // S, O read
+  PdTile tiles[kPdRing];
   uint32_t tmem;
-  int fail, began_here;
-  int64_t begun;
-  float qs[16], m[16], f[16], icw[16];
-  int pos[16];
-  float red[8][16], red2[8][16];
-  int64_t scratch[kPdThreads / 32 + 1 + 4];
+  int64_t begun;                             // unit at which the first item begins
+  float qs[2][16];                           // by item
+  int pos[2][16];
+  float f[4][16], icw[4][16], m[4][16], l[4][4][16];  // by tile
+  float fcur[16], icwcur[16], mcur[16];
+  float red[4][16], red2[4][16];
+  int64_t scratch[kPdThreads / 32 + 4];
 };
 
 // smem byte of coordinate i (0..D) of a token, before the 128-byte column is
@@ -146,14 +152,13 @@ __device__ __forceinline__ float pd_query(const PagedAttnArgs& a, const uint16_t
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
   const float inv = top > 0.0f ? 16256.0f / top : 0.0f;  // 127 * 128
-  const int n0 = (r / C::RQ) * 2 * C::RQ + r % C::RQ;     // column of slice 0
+  const int n0 = r, n1 = C::R + r;                        // columns of the slices
 #pragma unroll
   for (int w = 0; w < P::W; ++w) {
     const int v = __float2int_rn(Y[w] * inv);
     const int hi = (v + 64) >> 7, lo = v - hi * 128;
     const int b = pd_byte(L.k2 * P::W + w), col = b >> 7, in = b & 127;
     uint8_t* base = sq + col * C::NQS * 128;
-    const int n1 = n0 + C::RQ;
     base[n0 * 128 + (in ^ ((n0 & 7) << 4))] = uint8_t(hi);
     base[n1 * 128 + (in ^ ((n1 & 7) << 4))] = uint8_t(lo);
   }
@@ -203,414 +208,507 @@ __device__ __forceinline__ void pd_slices(const uint32_t* w, uint32_t& b0, uint3
   b2 = __byte_perm(__byte_perm(w[0], w[1], 0x0062), __byte_perm(w[2], w[3], 0x0062), 0x5410);
 }
 
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool named_or(int id, int threads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(p)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 template <int D, int R, int NG>
-__global__ void __launch_bounds__(kPdThreads + 32, Pd<D, R, NG>::BLOCKS)
+__global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     kvq_paged_decode_kernel(const PagedAttnArgs a, unsigned* status) {
   using C = Pd<D, R, NG>;
-  constexpr int RQ = C::RQ, AQ = C::AQ, KT = C::KT, KP = C::KP;
+  constexpr int KT = C::KT, KP = C::KP;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PdShared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = (warp >> 2) & 1;
-  const int row = tid & 127;  // smem row, or coordinate byte, of this thread
-  const uint32_t sdone = smem_u32(&sh.sdone), odone = smem_u32(&sh.odone);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
   if (tid == 0) {
-    mbar_init(sdone, 1);
-    mbar_init(odone, 1);
-    sh.fail = 0;
+    for (int i = 0; i < kPdRing; ++i) mbar_init(bar(sh.dfull[i]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(sh.kfull[i]), 4);
+      mbar_init(bar(sh.vfull[i]), 4);
+      mbar_init(bar(sh.pfull[i]), 4);
+      mbar_init(bar(sh.qfull[i]), 4);
+      mbar_init(bar(sh.sdone[i]), 1);
+      mbar_init(bar(sh.odone[i]), 1);
+      mbar_init(bar(sh.sfree[i]), 4);
+      mbar_init(bar(sh.ofree[i]), 4);
+    }
     fence_mbar_init();
   }
   pdl_wait();  // no global access before the previous kernel completes
-  const Run run = find_run<R, KT, kPdThreads + 32>(a, blockIdx.x, gridDim.x, sh.scratch, status);
+  const Run run = find_run<R, KT, kPdThreads>(a, blockIdx.x, gridDim.x, sh.scratch, status);
   JoinInfo* join = a.join + blockIdx.x;
-  if (run.begin == run.end) {
-    if (tid == 0) join->first_block = -1;
-    return;
-  }
-  const int n_tiles = int(run.end - run.begin);
+  if (tid == 0) join->first_block = -1;
+  if (run.begin == run.end) return;
+  const int n = int(run.end - run.begin);  // tiles
+  if (warp == 12) tmem_alloc(smem_u32(&sh.tmem), C::TMEM);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t tlane = tmem + (uint32_t(warp & 3) << 21);
+  bool ok = true;
+  // A wait that runs out is recorded and skipped from then on: every role still
+  // takes all its steps, so nobody is left at a barrier.
+  auto wait = [&](uint64_t& b, int phase) {
+    if (ok) ok = mbar_wait_bounded(smem_u32(&b), uint32_t(phase) & 1u);
+  };
+  auto arrive = [&](uint64_t& b) {  // one arrival for the warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&b));
+  };
 
-  if (warp == kPdThreads / 32) {
-    // ================= control: tile descriptions and MMA issue =================
-    tmem_alloc(smem_u32(&sh.tmem), C::TMEM);
+  if (warp == 12) {
+    // ---------------- control: descriptions, prefetches, MMAs ----------------
     Cursor<R, KT> c;
     c.seek(a, run.seq, run.off);
-    if (lane == 0) {
-      join->first_block = -1;
-      sh.begun = run.begin - c.tile;  // unit at which the first item begins
-      sh.began_here = c.tile == 0;
-    }
+    if (lane == 0) sh.begun = run.begin - c.tile;
     auto describe = [&](int i) {  // the cursor's tile as number i
-      PdTile& e = sh.tiles[i & 3];
+      PdTile& e = sh.tiles[i % kPdRing];
       const int t0 = (c.first + c.tile) * KT;
+      int64_t r = -1;
+      if (lane < KT / 16) {
+        const int64_t t = int64_t(t0) + lane * 16;
+        if (t < c.q.len) {
+          const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
+          if (page < 0 || page >= a.n_pages) {
+            flag_bad_index(status);
+          } else {
+            r = ((page * a.n_kv + c.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+            prefetch_l2(a.k_packed + r * (D / 2), 16 * (D / 2));
+            prefetch_l2(a.v_packed + r * (D / 2), 16 * (D / 2));
+            prefetch_l2(a.k_scales + r * NG, 64 * NG);
+            prefetch_l2(a.v_scales + r * NG, 64 * NG);
+          }
+        }
+        e.row[lane] = r;
+      }
+      const uint32_t have = __ballot_sync(kFull, r >= 0);
       if (lane == 0) {
+        const int row0 = c.qt * R;
+        const int rows = int(min(int64_t(R), int64_t(c.q.n) * a.n_q - row0));
+        const int pf = c.q.len - c.q.n + row0 / a.n_q;  // positions of the first and last row
+        const int pl = c.q.len - c.q.n + (row0 + rows - 1) / a.n_q;
         e.t0 = t0;
         e.len = c.q.len;
         e.c0 = c.q.c0;
         e.head = c.head;
-        e.row0 = c.qt * R;
-        e.rows = int(min(int64_t(R), int64_t(c.q.n) * a.n_q - int64_t(c.qt) * R));
-        e.p0 = c.q.len - c.q.n;
-        e.starts = c.tile == 0;
-        e.ends = c.tile + 1 == c.count;
+        e.row0 = row0;
+        e.rows = rows;
+        e.starts = i == 0 || c.tile == 0;
+        e.last = c.tile + 1 == c.count;
+        e.ends = e.last || i + 1 == n;
+        e.whole = t0 + KT - 1 <= pf && (a.window == 0 || t0 > pl - a.window) &&
+                  have == (KT == 256 ? 0xFFFFu : 0xFFu);
       }
-      if (lane < KT / 16) {
-        const int64_t t = int64_t(t0) + lane * 16;
-        int64_t r = -1;
-        if (t < c.q.len) {
-          const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
-          if (page < 0 || page >= a.n_pages)
-            flag_bad_index(status);
-          else
-            r = ((page * a.n_kv + c.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-        }
-        e.row[lane] = r;
-      }
-      if (i + 1 < n_tiles && ++c.tile == c.count) c.next_item(a);
+      arrive(sh.dfull[i % kPdRing]);
+      if (i + 1 < n && ++c.tile == c.count) c.next_item(a);
     };
-    for (int i = 0; i < min(3, n_tiles); ++i) describe(i);
-    tc_fence_before();
-    __syncthreads();  // descriptions, tensor memory
-    tc_fence_after();
-    const uint32_t tmem = sh.tmem;
-    for (int i = 0; i < n_tiles; ++i) {
-      __syncthreads();  // A
-      if (lane == 0) {
-        tc_fence_after();
-        constexpr uint32_t id = instr_desc(kAccS32, kFmtS8, kFmtS8, false, false, 128, C::NQS);
+    auto scores = [&](int i, int item) {
+      const uint32_t k = sbase + C::oK + (i & 1) * C::TILE;
+      const uint32_t q = sbase + C::oQ + (item & 1) * C::QB;
+      constexpr uint32_t id = instr_desc(kAccS32, kFmtS8, kFmtS8, false, false, 128, C::NQS);
+      tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < C::SBLK; ++b) {
-          const int half = b / NG, j = b % NG;
+      for (int b = 0; b < C::SBLK; ++b) {
+        const int half = b / NG, j = b % NG;
 #pragma unroll
-          for (int k = 0; k < C::G; k += 32) {
-            const int byte = j * C::G + k;  // in the token's bytes
-            const int abyte = C::TPR == 2 ? half * 64 + byte : byte;
-            mma_i8(tmem + b * C::NQS,
-                   smem_desc(sbase + C::oK + (abyte >> 7) * 16384 + (abyte & 127), 16, 1024, kSw128),
-                   smem_desc(sbase + C::oQ + (byte >> 7) * (C::NQS * 128) + (byte & 127), 16, 1024,
-                             kSw128),
-                   id, k > 0);
+        for (int x = 0; x < C::G; x += 32) {
+          const int byte = j * C::G + x;  // in the token's bytes
+          const int abyte = C::TPR == 2 ? half * 64 + byte : byte;
+          mma_i8(tmem + (i & 1) * C::SCOLS + b * C::NQS,
+                 smem_desc(k + (abyte >> 7) * 16384 + (abyte & 127), 16, 1024, kSw128),
+                 smem_desc(q + (byte >> 7) * (C::NQS * 128) + (byte & 127), 16, 1024, kSw128), id,
+                 x > 0);
+        }
+      }
+      mma_commit(bar(sh.sdone[i & 1]));
+    };
+    auto values = [&](int i) {
+      const uint32_t v = sbase + C::oV + (i & 1) * C::TILE, p = sbase + C::oP + (i & 1) * C::PB;
+      // one MMA for all groups of a 128-coordinate block
+      constexpr uint32_t id = instr_desc(kAccS32, kFmtS8, kFmtU8, true, true, 128, C::NGM * C::NP);
+      tc_fence_after();
+#pragma unroll
+      for (int mt = 0; mt < C::NCH; ++mt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          mma_i8(tmem + 2 * C::SCOLS + (i % C::OBUF) * C::OCOLS + mt * C::NGM * C::NP,
+                 smem_desc(v + mt * 16384 + x * 4096, 16, 1024, kSw128),
+                 smem_desc(p + (NG == 1 ? 0 : mt * C::NGM * 128 * C::NP) + x * 32 * C::NP,
+                           128 * C::NP, 8 * C::NP, C::PSW),
+                 id, x > 0);
+      mma_commit(bar(sh.odone[i & 1]));
+    };
+    int item = 0;  // of the next tile whose scores are issued
+    auto issue_scores = [&](int i) {
+      PdTile& e = sh.tiles[i % kPdRing];
+      if (i > 0 && e.starts) ++item;
+      if (e.starts) wait(sh.qfull[item & 1], item >> 1);
+      wait(sh.kfull[i & 1], i >> 1);
+      if (i >= 2) wait(sh.sfree[i & 1], (i >> 1) - 1);
+      if (lane == 0) scores(i, item);
+      __syncwarp();
+    };
+    for (int i = 0; i < min(6, n); ++i) describe(i);
+    issue_scores(0);
+    for (int i = 0; i < n; ++i) {
+      if (i + 1 < n) issue_scores(i + 1);
+      wait(sh.vfull[i & 1], i >> 1);
+      wait(sh.pfull[i & 1], i >> 1);
+      if (i >= C::OBUF) wait(sh.ofree[i % C::OBUF], (i / C::OBUF) - 1);
+      if (lane == 0) values(i);
+      __syncwarp();
+      if (i + 6 < n) describe(i + 6);
+    }
+  } else if (warp >= 8) {
+    // ---------------- expansion: packed codes -> 16 c bytes ----------------
+    const int et = tid - 256;
+    uint4 kreg[KP], vreg[KP];
+    auto load = [&](int i, const uint8_t* base, uint4 (&w)[KP]) {
+      const PdTile& e = sh.tiles[i % kPdRing];
+#pragma unroll
+      for (int k = 0; k < KP; ++k) {
+        const int p = et + 128 * k, t = p / (D / 32);
+        const int64_t r = e.row[t >> 4];
+        w[k] = make_uint4(0, 0, 0, 0);
+        if (r >= 0)
+          w[k] = __ldg(reinterpret_cast<const uint4*>(base + r * (D / 2)) +
+                       (t & 15) * (D / 32) + p % (D / 32));
+      }
+    };
+    auto expand = [&](const uint4 (&w)[KP], uint32_t tile) {
+#pragma unroll
+      for (int k = 0; k < KP; ++k) {
+        const int p = et + 128 * k, t = p / (D / 32);
+        const int r = t & 127;
+        const int byte = (t >> 7) * 64 + p % (D / 32) * 32;  // in the row's bytes
+        const uint32_t base = tile + uint32_t(byte >> 7) * 16384 + uint32_t(r) * 128;
+        const uint32_t c0 = (uint32_t(byte & 127) >> 4) ^ uint32_t(r & 7), c1 = c0 ^ 1u;
+        constexpr uint32_t H = 0xF0F0F0F0u;
+        sts128(base + c0 * 16, (w[k].x << 4) & H, w[k].x & H, (w[k].y << 4) & H, w[k].y & H);
+        sts128(base + c1 * 16, (w[k].z << 4) & H, w[k].z & H, (w[k].w << 4) & H, w[k].w & H);
+      }
+      fence_proxy_async_smem();
+    };
+    wait(sh.dfull[0], 0);
+    load(0, a.k_packed, kreg);
+    load(0, a.v_packed, vreg);
+    for (int i = 0; i < n; ++i) {
+      if (i >= 2) wait(sh.sdone[i & 1], (i >> 1) - 1);
+      expand(kreg, sbase + C::oK + (i & 1) * C::TILE);
+      arrive(sh.kfull[i & 1]);
+      if (i + 1 < n) {
+        wait(sh.dfull[(i + 1) % kPdRing], (i + 1) / kPdRing);
+        load(i + 1, a.k_packed, kreg);
+      }
+      if (i >= 2) wait(sh.odone[i & 1], (i >> 1) - 1);
+      expand(vreg, sbase + C::oV + (i & 1) * C::TILE);
+      arrive(sh.vfull[i & 1]);
+      if (i + 1 < n) load(i + 1, a.v_packed, vreg);
+    }
+  } else if (warp < 4) {
+    // ---------------- softmax: a token's scores -> weights ----------------
+    const int row = tid;  // smem row; tokens row (and row + 128 at d = 64) of the tile
+    constexpr int TPR = C::TPR;
+    float m[R], l[R], cw[R];
+    float ks[TPR][NG], vs[TPR][NG];
+    bool seen[TPR], fresh = true;
+    auto load_scales = [&](int i) {
+      const PdTile& e = sh.tiles[i % kPdRing];
+#pragma unroll
+      for (int h = 0; h < TPR; ++h) {
+        const int tl = row + 128 * h;
+        const int64_t r = e.row[tl >> 4];
+        seen[h] = r >= 0 && e.t0 + tl < e.len;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) ks[h][j] = vs[h][j] = 0.0f;
+        if (seen[h]) {
+          const float* kp = a.k_scales + (r + (tl & 15)) * NG;
+          const float* vp = a.v_scales + (r + (tl & 15)) * NG;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) ks[h][j] = __ldg(kp + j), vs[h][j] = __ldg(vp + j);
+        }
+      }
+    };
+    int item = -1;
+    wait(sh.dfull[0], 0);
+    load_scales(0);
+    for (int i = 0; i < n; ++i) {
+      const PdTile& e = sh.tiles[i % kPdRing];
+      const int rows = e.rows;
+      if (e.starts) {
+        ++item;
+        wait(sh.qfull[item & 1], item >> 1);
+#pragma unroll
+        for (int r = 0; r < R; ++r) m[r] = -3e38f, l[r] = 0.0f, cw[r] = 1.0f;
+        fresh = true;
+      }
+      const float* qs = sh.qs[item & 1];
+      float vmax[TPR];
+#pragma unroll
+      for (int h = 0; h < TPR; ++h) {
+        vmax[h] = vs[h][0];
+#pragma unroll
+        for (int j = 1; j < NG; ++j) vmax[h] = fmaxf(vmax[h], vs[h][j]);
+      }
+      wait(sh.sdone[i & 1], i >> 1);
+      tc_fence_after();
+      float s[TPR][R];
+#pragma unroll
+      for (int h = 0; h < TPR; ++h)
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[h][r] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < C::SBLK; ++b) {
+        const int h = b / NG, j = b % NG;
+        uint32_t x[2 * R];
+        tmem_ld<2 * R>(tlane + (i & 1) * C::SCOLS + b * C::NQS, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (r < rows)
+            s[h][r] = fmaf(ks[h][j], float(int(x[r]) * 128 + int(x[R + r])), s[h][r]);
+      }
+      tc_fence_before();
+      arrive(sh.sfree[i & 1]);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < rows) {
+          const float q = qs[r];
+#pragma unroll
+          for (int h = 0; h < TPR; ++h) s[h][r] *= q;
+        }
+      if (!e.whole) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int p = sh.pos[item & 1][r];
+#pragma unroll
+          for (int h = 0; h < TPR; ++h) {
+            const int t = e.t0 + row + 128 * h;
+            if (!seen[h] || t > p || (a.window > 0 && t <= p - a.window)) s[h][r] = -INFINITY;
           }
         }
-        mma_commit(sdone);
       }
-      __syncwarp();
-      const bool ends = sh.tiles[i & 3].ends || i + 1 == n_tiles;
-      if (i + 3 < n_tiles) describe(i + 3);
-      if (__syncthreads_or(0)) {  // B
-        if (sh.fail) break;
-        __syncthreads();
-        __syncthreads();
-        __syncthreads();
-      }
-      if (lane == 0) {
-        tc_fence_after();
-        // one MMA for all groups of a 128-coordinate block
-        constexpr uint32_t id =
-            instr_desc(kAccS32, kFmtS8, kFmtU8, true, true, 128, C::NGM * C::NP);
-#pragma unroll
-        for (int mt = 0; mt < C::NCH; ++mt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_i8(tmem + mt * C::NGM * C::NP,
-                   smem_desc(sbase + C::oV + mt * 16384 + k * 4096, 16, 1024, kSw128),
-                   smem_desc(sbase + C::oP + (NG == 1 ? 0 : mt * C::NGM * 128 * C::NP) +
-                                 k * 32 * C::NP,
-                             128 * C::NP, 8 * C::NP, C::PSW),
-                   id, k > 0);
-        mma_commit(odone);
-      }
-      __syncwarp();
-      if (ends) __syncthreads();  // results of the item
-    }
-    __syncthreads();  // every read of tensor memory is done
-    tmem_free(tmem, C::TMEM);
-    return;
-  }
 
-  // ========================== the eight other warps ==========================
-  __syncthreads();  // descriptions, tensor memory
-  tc_fence_after();
-  const uint32_t tlane = sh.tmem + (uint32_t(warp & 3) << 21);
-  const int tl = C::TPR == 2 ? wg * 128 + row : row;  // token of this thread's scores
-  const int q0 = C::TPR == 2 ? 0 : wg * RQ;           // its first query row
-  const int half = C::TPR == 2 ? row >> 6 : 0;        // of the accumulators: d = 64 half,
-  const int crd = C::TPR == 2 ? row & 63 : row;       // coordinate byte,
-  const int a0 = D == 256 ? 0 : wg * AQ;              // first query row
-
-  // Packed codes of a tile in registers: piece tid + 256 k of 16 bytes, each
-  // loaded a tile's time before it is expanded.
-  uint4 kreg[KP], vreg[KP];
-  float ks[NG], vs[NG];
-  bool seen;
-  auto load_codes = [&](int i, const uint8_t* base, uint4 (&w)[KP]) {
-    const PdTile& e = sh.tiles[i & 3];
+      const uint32_t pt = sbase + C::oP + (i & 1) * C::PB;
+      if (i >= 2) wait(sh.odone[i & 1], (i >> 1) - 1);  // P is free
+      auto weights = [&]() {
+        bool over = false;
 #pragma unroll
-    for (int k = 0; k < KP; ++k) {
-      const int p = tid + kPdThreads * k, t = p / (D / 32);
-      const int64_t r = e.row[t >> 4];
-      w[k] = make_uint4(0, 0, 0, 0);
-      if (r >= 0)
-        w[k] = __ldg(reinterpret_cast<const uint4*>(base + (r + (t & 15)) * (D / 2)) + p % (D / 32));
-    }
-  };
-  auto load_scales = [&](int i) {
-    const PdTile& e = sh.tiles[i & 3];
-    const int64_t r = e.row[tl >> 4];
-    seen = r >= 0 && e.t0 + tl < e.len;
+        for (int h = 0; h < TPR; ++h) {
+          float p[R];
 #pragma unroll
-    for (int j = 0; j < NG; ++j) ks[j] = vs[j] = 0.0f;
-    if (seen) {
-      const float* kp = a.k_scales + (r + (tl & 15)) * NG;
-      const float* vp = a.v_scales + (r + (tl & 15)) * NG;
+          for (int r = 0; r < R; ++r) {
+            p[r] = 0.0f;
+            if (r < rows) {
+              const float x = s[h][r] - m[r];
+              p[r] = ex2(x);
+              l[r] += p[r];
+              over = over || x > 7.0f || p[r] * vmax[h] * cw[r] > 127.0f;
+            }
+          }
 #pragma unroll
-      for (int j = 0; j < NG; ++j) ks[j] = __ldg(kp + j), vs[j] = __ldg(vp + j);
-    }
-  };
-  // -> 16 c bytes in a swizzled tile
-  auto expand = [&](const uint4 (&w)[KP], uint32_t tile) {
+          for (int j = 0; j < NG; ++j) {
+            constexpr int NB = 3 * R / 4, NBR = (NB + 3) / 4 * 4;
+            uint32_t w[R], b[NBR];
 #pragma unroll
-    for (int k = 0; k < KP; ++k) {
-      const int p = tid + kPdThreads * k, t = p / (D / 32);
-      const int r = t & 127;
-      const int byte = (t >> 7) * 64 + p % (D / 32) * 32;  // in the row's bytes
-      const uint32_t base = tile + uint32_t(byte >> 7) * 16384 + uint32_t(r) * 128;
-      const uint32_t c0 = (uint32_t(byte & 127) >> 4) ^ uint32_t(r & 7), c1 = c0 ^ 1u;
-      constexpr uint32_t H = 0xF0F0F0F0u;
-      sts128(base + c0 * 16, (w[k].x << 4) & H, w[k].x & H, (w[k].y << 4) & H, w[k].y & H);
-      sts128(base + c1 * 16, (w[k].z << 4) & H, w[k].z & H, (w[k].w << 4) & H, w[k].w & H);
-    }
-  };
-
-  float m[RQ], l[RQ], cw[RQ], acc[AQ];
-  bool fresh = true;
-  auto start_item = [&](const PdTile& e) {
+            for (int r = NB; r < NBR; ++r) b[r] = 0u;
 #pragma unroll
-    for (int r = 0; r < RQ; ++r) m[r] = -3e38f, l[r] = 0.0f, cw[r] = 1.0f;
+            for (int r = 0; r < R; ++r)
+              w[r] = __float_as_uint(fmaf(p[r] * vs[h][j], cw[r] * 65536.0f, 8388608.0f));
 #pragma unroll
-    for (int r = 0; r < AQ; ++r) acc[r] = 0.0f;
-    fresh = true;
-    for (int r = warp; r < e.rows; r += kPdThreads / 32) {
-      const int tok = (e.row0 + r) / a.n_q;
-      const uint16_t* src = a.q + (int64_t(e.c0) + tok) * a.q_stride +
-                            (int64_t(e.head) * a.n_q + (e.row0 + r - tok * a.n_q)) * D;
-      const float qs = a.rot == kRotSRFT ? pd_query<C, kRotSRFT>(a, src, smem + C::oQ, r, lane)
-                                         : pd_query<C, kRotSRHT>(a, src, smem + C::oQ, r, lane);
-      if (lane == 0) {
-        sh.qs[r] = qs;
-        sh.pos[r] = e.p0 + tok;
-        sh.m[r] = -3e38f;
-      }
-    }
-  };
-
-  load_codes(0, a.k_packed, kreg);
-  load_codes(0, a.v_packed, vreg);
-  load_scales(0);
-  start_item(sh.tiles[0]);
-  expand(kreg, sbase + C::oK);
-  if (n_tiles > 1) load_codes(1, a.k_packed, kreg);
-  fence_proxy_async_smem();
-  bool began_here = sh.began_here, ok = true;
-
-  for (int i = 0; i < n_tiles; ++i) {
-    const PdTile& e = sh.tiles[i & 3];
-    const uint32_t par = uint32_t(i) & 1u;
-    const bool more = i + 1 < n_tiles;
-    __syncthreads();  // A: K and the queries are in shared memory, O is read
-    expand(vreg, sbase + C::oV);
-    if (more) load_codes(i + 1, a.v_packed, vreg);
-
-    // ---- scores of this thread's token ----
-    const int nr = min(max(e.rows - q0, 0), RQ);
-    const int t = e.t0 + tl;
-    const int pf = e.p0 + e.row0 / a.n_q;  // positions of the first and the last row
-    const int pl = e.p0 + (e.row0 + e.rows - 1) / a.n_q;
-    const bool whole = e.t0 + KT - 1 <= pf && (a.window == 0 || e.t0 > pl - a.window);
-    const float vmax = [&] {
-      float x = vs[0];
+            for (int r = 0; r < R / 4; ++r)
+              pd_slices(w + 4 * r, b[r], b[R / 4 + r], b[R / 2 + r]);
+            // row of NP bytes, a run of PW for each of its tokens; 16-byte pieces swizzled
+            const uint32_t base = pt + uint32_t(j * 128 + row) * C::NP;
+            const uint32_t x =
+                C::NP == 32 ? (row >> 2) & 1 : (C::NP == 64 ? (row >> 1) & 3 : row & 7);
 #pragma unroll
-      for (int j = 1; j < NG; ++j) x = fmaxf(x, vs[j]);
-      return x;
-    }();
-    ok = mbar_wait_bounded(sdone, par) && ok;
-    tc_fence_after();
-    float s[RQ];
-    {
-      uint32_t x[NG][2 * RQ];
-#pragma unroll
-      for (int j = 0; j < NG; ++j)
-        tmem_ld<2 * RQ>(tlane + uint32_t(((C::TPR == 2 ? wg * NG : 0) + j) * C::NQS + q0 * 2), x[j]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int r = 0; r < RQ; ++r)
-        if (r < nr) {
-          float v = 0.0f;
-#pragma unroll
-          for (int j = 0; j < NG; ++j)
-            v = fmaf(ks[j], float(int(x[j][r]) * 128 + int(x[j][RQ + r])), v);
-          s[r] = v * sh.qs[q0 + r];
-          if (!seen) s[r] = -INFINITY;
-          if (!whole) {
-            const int p = sh.pos[q0 + r];
-            if (t > p || (a.window > 0 && t <= p - a.window)) s[r] = -INFINITY;
+            for (int k = 0; k < NBR; k += 4)
+              sts128(base + ((uint32_t(h * (C::PW / 16) + k / 4) ^ x) * 16), b[k], b[k + 1],
+                     b[k + 2], b[k + 3]);
           }
         }
-    }
-
-    // ---- weights and their slices ----
-    auto weights = [&]() {
-      bool over = false;
-      float p[RQ];
+        fence_proxy_async_smem();
+        return over;
+      };
+      float lold[R];
 #pragma unroll
-      for (int r = 0; r < RQ; ++r) {
-        p[r] = 0.0f;
-        if (r < nr) {
-          const float x = s[r] - m[r];
-          p[r] = ex2(x);
-          l[r] += p[r];
-          over = over || x > 7.0f || p[r] * vmax * cw[r] > 127.0f;
+      for (int r = 0; r < R; ++r) lold[r] = l[r];
+      const bool over = fresh ? true : weights();
+      const bool slow = named_or(1, 128, over);
+      if (slow) {
+        // the tile's maxima -> new references; then the weights once more
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          l[r] = lold[r];
+          float x = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < TPR; ++h) x = fmaxf(x, s[h][r]);
+          if (r >= rows) x = -INFINITY;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+          if (lane == 0) sh.red[warp][r] = x;
+        }
+        named_sync(1, 128);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float mn = m[r];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) mn = fmaxf(mn, sh.red[w][r]);
+          const float f = ex2(m[r] - mn);
+          l[r] *= f;
+          m[r] = mn;
+          float x = 0.0f;
+#pragma unroll
+          for (int h = 0; h < TPR; ++h)
+            if (r < rows) x = fmaxf(x, ex2(s[h][r] - mn) * vmax[h]);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+          if (lane == 0) sh.red2[warp][r] = x;
+          if (row == 0) sh.fcur[r] = f, sh.mcur[r] = mn;
+        }
+        named_sync(1, 128);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float x = 0.0f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.red2[w][r]);
+          // the power of two that brings the largest into [1/2, 1)
+          const int ex = min(max(253 - int(__float_as_uint(x) >> 23), 1), 237);
+          cw[r] = __uint_as_float(uint32_t(ex) << 23);
+          if (row == 0) sh.icwcur[r] = __uint_as_float(uint32_t(254 - ex) << 23);
+        }
+        weights();
+      }
+      fresh = false;
+      __syncwarp();
+      if (warp == 0 && lane < R) {  // what the accumulation needs to know of this tile
+        sh.f[i & 3][lane] = slow ? sh.fcur[lane] : 1.0f;
+        sh.icw[i & 3][lane] = sh.icwcur[lane] * (1.0f / 1048576.0f);
+        sh.m[i & 3][lane] = sh.mcur[lane];
+      }
+      if (e.ends) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float x = l[r];
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+          if (lane == 0) sh.l[i & 3][warp][r] = x;
         }
       }
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        uint32_t w[RQ];
-#pragma unroll
-        for (int r = 0; r < RQ; ++r)
-          w[r] = __float_as_uint(fmaf(p[r] * vs[j], cw[r] * 65536.0f, 8388608.0f));
-        constexpr int NB = 3 * RQ / 4;
-        uint32_t b[(NB + 3) / 4 * 4];
-#pragma unroll
-        for (int r = NB; r < (NB + 3) / 4 * 4; ++r) b[r] = 0u;
-#pragma unroll
-        for (int r = 0; r < RQ / 4; ++r)
-          pd_slices(w + 4 * r, b[r], b[RQ / 4 + r], b[RQ / 2 + r]);
-        // row of 2 PW bytes, this thread's half of it; 16-byte pieces swizzled
-        const uint32_t base = sbase + C::oP + uint32_t(j * 128 + row) * C::NP;
-        const uint32_t x = C::NP == 32 ? (row >> 2) & 1 : (C::NP == 64 ? (row >> 1) & 3 : row & 7);
-#pragma unroll
-        for (int k = 0; k < NB; k += 4)
-          sts128(base + ((uint32_t(wg * (C::PW / 16) + k / 4) ^ x) * 16), b[k], b[k + 1], b[k + 2],
-                 b[k + 3]);
+      arrive(sh.pfull[i & 1]);
+      if (i + 1 < n) {
+        wait(sh.dfull[(i + 1) % kPdRing], (i + 1) / kPdRing);
+        load_scales(i + 1);
       }
-      fence_proxy_async_smem();  // V's stores too
-      return over;
+    }
+  } else {
+    // ---------- accumulation, results, and the queries of the next items ----------
+    const int aw = warp - 4, row = tid - 128;  // row: coordinate byte
+    const int half = C::TPR == 2 ? row >> 6 : 0, crd = C::TPR == 2 ? row & 63 : row;
+    Cursor<R, KT> qc;
+    qc.seek(a, run.seq, run.off);
+    int64_t next = run.begin - qc.tile + qc.count;  // unit of the item after qc's
+    auto prepare = [&](int item) {                  // qc's queries
+      const int row0 = qc.qt * R, b = item & 1;
+      const int rows = int(min(int64_t(R), int64_t(qc.q.n) * a.n_q - row0));
+      for (int r = aw; r < rows; r += 4) {
+        const int tok = (row0 + r) / a.n_q;
+        const uint16_t* src = a.q + (int64_t(qc.q.c0) + tok) * a.q_stride +
+                              (int64_t(qc.head) * a.n_q + (row0 + r - tok * a.n_q)) * D;
+        uint8_t* sq = smem + C::oQ + b * C::QB;
+        const float qs = a.rot == kRotSRFT ? pd_query<C, kRotSRFT>(a, src, sq, r, lane)
+                                           : pd_query<C, kRotSRHT>(a, src, sq, r, lane);
+        if (lane == 0) {
+          sh.qs[b][r] = qs;
+          sh.pos[b][r] = qc.q.len - qc.q.n + tok;
+        }
+      }
+      fence_proxy_async_smem();
+      arrive(sh.qfull[b]);
     };
-    float lold[RQ];
+    auto prepare_next = [&](int item) {
+      if (next >= run.end) return;
+      qc.next_item(a);
+      next += qc.count;
+      prepare(item);
+    };
+    prepare(0);
+    prepare_next(1);
+    int item = 0;
+    float acc[C::NCH][R];
+    for (int i = 0; i < n; ++i) {
+      wait(sh.dfull[i % kPdRing], i / kPdRing);
+      const PdTile& e = sh.tiles[i % kPdRing];
+      if (e.starts) {
 #pragma unroll
-    for (int r = 0; r < RQ; ++r) lold[r] = l[r];
-    const bool over = fresh ? true : weights();
-    if (!ok) sh.fail = 1;
-    tc_fence_before();
-    const bool slow = __syncthreads_or(over || !ok);  // B: V and P are in shared memory
-    if (slow) {
-      if (sh.fail) break;  // uniform: written before the barrier
-      // the tile's maxima -> new references; then the weights once more
+        for (int c = 0; c < C::NCH; ++c)
 #pragma unroll
-      for (int r = 0; r < RQ; ++r) {
-        l[r] = lold[r];
-        float x = r < nr ? s[r] : -INFINITY;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-        if (lane == 0) sh.red[warp][r] = x;
+          for (int r = 0; r < R; ++r) acc[c][r] = 0.0f;
       }
-      __syncthreads();
+      const int rows = e.rows;
+      wait(sh.odone[i & 1], i >> 1);
+      tc_fence_after();
 #pragma unroll
-      for (int r = 0; r < RQ; ++r) {
-        float mn = m[r];
+      for (int c = 0; c < C::NCH; ++c) {
+        const int blk = D == 256 ? c * C::NGM + crd / (C::G > 128 ? 128 : C::G) : crd / C::G;
+        const uint32_t at = tlane + 2 * C::SCOLS + (i % C::OBUF) * C::OCOLS +
+                            uint32_t(blk * C::NP + half * C::PW);
+        uint32_t x0[R], x1[R], x2[R];
+        tmem_ld<R>(at, x0);
+        tmem_ld<R>(at + R, x1);
+        tmem_ld<R>(at + 2 * R, x2);
+        tmem_wait_ld();
 #pragma unroll
-        for (int w = 0; w < 4; ++w) mn = fmaxf(mn, sh.red[wg * 4 + w][r]);
-        if constexpr (C::TPR == 2) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) mn = fmaxf(mn, sh.red[(wg ^ 1) * 4 + w][r]);
-        }
-        const float f = ex2(m[r] - mn);
-        l[r] *= f;
-        m[r] = mn;
-        float x = r < nr ? ex2(s[r] - mn) * vmax : 0.0f;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-        if (lane == 0) sh.red2[warp][r] = x;
-        if (row == 0 && (C::TPR == 1 || wg == 0)) {
-          sh.f[q0 + r] = f;
-          sh.m[q0 + r] = mn;
-        }
+        for (int r = 0; r < R; ++r)
+          if (r < rows) {
+            const float v = fmaf(float(int(x2[r])), 65536.0f, float(int(x1[r]) * 256 + int(x0[r])));
+            acc[c][r] = fmaf(v, sh.icw[i & 3][r], acc[c][r] * sh.f[i & 3][r]);
+          }
       }
-      __syncthreads();
-#pragma unroll
-      for (int r = 0; r < RQ; ++r) {
-        float x = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.red2[wg * 4 + w][r]);
-        if constexpr (C::TPR == 2) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.red2[(wg ^ 1) * 4 + w][r]);
-        }
-        // the power of two that brings the largest into [1/2, 1)
-        const int ex = min(max(253 - int(__float_as_uint(x) >> 23), 1), 237);
-        cw[r] = __uint_as_float(uint32_t(ex) << 23);
-        if (row == 0 && (C::TPR == 1 || wg == 0))
-          sh.icw[q0 + r] = __uint_as_float(uint32_t(254 - ex) << 23);
+      float lsum = 0.0f, mref = 0.0f;
+      if (e.ends && lane < R) {  // of query row `lane`
+        lsum = sh.l[i & 3][0][lane] + sh.l[i & 3][1][lane] + sh.l[i & 3][2][lane] +
+               sh.l[i & 3][3][lane];
+        mref = sh.m[i & 3][lane];
       }
-      weights();
-      __syncthreads();
-    }
-    fresh = false;
-    if (more) {
-      load_scales(i + 1);
-      expand(kreg, sbase + C::oK);
-      if (i + 2 < n_tiles) load_codes(i + 2, a.k_packed, kreg);
-    }
+      tc_fence_before();
+      arrive(sh.ofree[i % C::OBUF]);
+      if (!e.ends) continue;
 
-    // ---- accumulate the tile's O: this thread's coordinate, its query rows ----
-    ok = mbar_wait_bounded(odone, par) && ok;
-    tc_fence_after();
-    // The columns of a query row: segment of P (the byte's half at d = 64, wg at
-    // d = 128, both in turn at d = 256), slice, row in the segment.
-    constexpr int HN = D == 256 ? 2 : 1, CN = AQ / HN;
-    const int blk = D == 256 ? wg * C::NGM + crd / (C::G > 128 ? 128 : C::G) : crd / C::G;
+      // ---- end of the item, or of the block's share of it ----
+      const bool began_here = item > 0 || sh.begun == run.begin;
+      const bool complete = e.last && began_here;
+      float* ob = reinterpret_cast<float*>(smem + C::oO);
+      named_sync(2, 128);  // the result before is read
 #pragma unroll
-    for (int h = 0; h < HN; ++h) {
-      const int seg = D == 64 ? half : (D == 128 ? wg : h);
-      const uint32_t at =
-          tlane + uint32_t(blk * C::NP + seg * C::PW + (D == 64 ? wg * AQ : 0));
-      uint32_t x0[CN], x1[CN], x2[CN];
-      tmem_ld<CN>(at, x0);
-      tmem_ld<CN>(at + RQ, x1);
-      tmem_ld<CN>(at + 2 * RQ, x2);
-      tmem_wait_ld();
+      for (int c = 0; c < C::NCH; ++c)
 #pragma unroll
-      for (int k = 0; k < CN; ++k) {
-        const int ai = h * CN + k, r = a0 + ai;
-        if (r < e.rows) {
-          const float v = fmaf(float(int(x2[k])), 65536.0f, float(int(x1[k]) * 256 + int(x0[k])));
-          if (slow) acc[ai] *= sh.f[r];
-          acc[ai] = fmaf(v, sh.icw[r] * (1.0f / 1048576.0f), acc[ai]);
-        }
-      }
-    }
-    tc_fence_before();
-
-    // ---- end of the item, or of the block's share of it ----
-    if (e.ends || !more) {
-#pragma unroll
-      for (int r = 0; r < RQ; ++r) {
-        float x = l[r];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
-        if (lane == 0) sh.red[warp][r] = x;
-      }
-      const bool complete = e.ends && began_here;
-      const int dim = D == 256 ? wg * 128 + pd_dim(row) : pd_dim(crd);
-      float* ob = reinterpret_cast<float*>(smem + C::oP);
-#pragma unroll
-      for (int k = 0; k < AQ; ++k) ob[(half * R + a0 + k) * D + dim] = acc[k];
-      __syncthreads();
-      for (int r = warp; r < e.rows; r += kPdThreads / 32) {
-        float ls = 0.0f;
-        const int w0 = C::TPR == 2 ? 0 : (r / RQ) * 4;
-        for (int w = 0; w < (C::TPR == 2 ? 8 : 4); ++w) ls += sh.red[w0 + w][r % RQ];
+        for (int r = 0; r < R; ++r)
+          ob[(half * R + r) * D + c * 128 + pd_dim(crd)] = acc[c][r];
+      named_sync(2, 128);
+      for (int r = aw; r < rows; r += 4) {
+        const float ls = __shfl_sync(kFull, lsum, r);
         auto value = [&](int d) {
           float v = ob[r * D + d];
           if constexpr (C::TPR == 2) v += ob[(R + r) * D + d];
@@ -637,27 +735,27 @@ __global__ void __launch_bounds__(kPdThreads + 32, Pd<D, R, NG>::BLOCKS)
           }
         } else {
           float* slot = part_slot<D, R>(a, blockIdx.x, began_here ? 1 : 0);
-          if (lane == 0) slot[r] = sh.m[r], slot[R + r] = ls;
+          const float mr = __shfl_sync(kFull, mref, r);
+          if (lane == 0) slot[r] = mr, slot[R + r] = ls;
           for (int d = lane; d < D; d += 32) slot[2 * R + r * D + d] = value(d);
         }
       }
-      if (e.ends && !began_here && tid == 0) {
+      if (e.last && !began_here && tid == 128) {
         join->c0 = e.c0;
         join->head = e.head;
         join->row0 = e.row0;
-        join->rows = e.rows;
+        join->rows = rows;
         join->first_block = block_of(sh.begun, run.total, run.blocks);
       }
-      if (more) {
-        began_here = true;
-        start_item(sh.tiles[(i + 1) & 3]);
-      }
+      prepare_next(item + 2);
+      ++item;
     }
-    fence_proxy_async_smem();  // K's and the queries' stores
   }
-  if (!ok) atomicOr(status, kPagedTimeout);
+  if (!ok && lane == 0) atomicOr(status, kPagedTimeout);
   pdl_release();
+  tc_fence_before();
   __syncthreads();  // every read of tensor memory is done
+  if (warp == 12) tmem_free(tmem, C::TMEM);
 }
 
 // Joins the partial results of items that several blocks shared: block b the
