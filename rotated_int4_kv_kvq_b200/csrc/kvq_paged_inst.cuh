@@ -123,10 +123,10 @@ cudaError_t few_rows_group(const PagedAttnArgs& a, int sm_count, cudaStream_t st
     case 1: return few_rows<D, R, 1>(a, sm_count, stream, st);
     case 2: return few_rows<D, R, 2>(a, sm_count, stream, st);
     case 4:
-      if constexpr (D == 128 || (D == 256 && R == 8)) return few_rows<D, R, 4>(a, sm_count, stream, st);
+      if constexpr (D == 128 || (D == 256 && R <= 8)) return few_rows<D, R, 4>(a, sm_count, stream, st);
       break;
     case 8:
-      if constexpr (D >= 256 && R == 8) return few_rows<D, R, 8>(a, sm_count, stream, st);
+      if constexpr (D >= 256 && R <= 8) return few_rows<D, R, 8>(a, sm_count, stream, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -174,9 +174,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int max_q_len, int sm_coun
   cudaError_t e = detail::paged_status_ptr(&st);
   if (e != cudaSuccess) return e;
   const int r = few_rows_item(D, a.group, int64_t(max_q_len) * a.n_q);
-  if constexpr (D == 64) {
-    if (r == 4) return detail::few_rows_group<D, 4>(a, sm_count, stream, st);
-  }
+  if (r == 4) return detail::few_rows_group<D, 4>(a, sm_count, stream, st);
   return r == 8 ? detail::few_rows_group<D, 8>(a, sm_count, stream, st)
                 : detail::few_rows_group<D, 16>(a, sm_count, stream, st);
 }

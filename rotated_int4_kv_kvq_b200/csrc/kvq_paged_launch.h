@@ -70,7 +70,7 @@ struct PagedAttnArgs {
 // KV head: fewer columns cost less of everything, and 16 do not fit shared
 // and tensor memory with 4 or 8 groups of a 256-value row.
 constexpr int few_rows_item(int d, int group, int64_t rows) {
-  return d == 64 && rows <= 4 ? 4 : (rows <= 8 || (d == 256 && group <= 64) ? 8 : 16);
+  return rows <= 4 ? 4 : (rows <= 8 || (d == 256 && group <= 64) ? 8 : 16);
 }
 constexpr int64_t kMaxBlocks = 148 * 4;  // of the few-rows kernel
 constexpr int64_t few_rows_workspace(int d) {

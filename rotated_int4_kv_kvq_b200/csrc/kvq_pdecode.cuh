@@ -30,9 +30,8 @@
 // A tile is 128 smem rows of 128 bytes (two tokens a row at d = 64, half a
 // token at d = 256).  A block is a pipeline of roles: four warps expand codes
 // (global -> registers a tile ahead -> bytes), four turn scores into weights,
-// four accumulate results and prepare the queries of the next item, one looks
-// pages up, prefetches into L2 and issues the MMAs.  Operands, scores and
-// results are double-buffered, so the roles work on neighbouring tiles at once.
+// four accumulate results and prepare the queries of the next item, one issues
+// the MMAs, one looks the pages up.  Operands, scores and results are double-buffered, so the roles work on neighbouring tiles at once.
 #pragma once
 
 #include "kvq_sched.cuh"
@@ -41,7 +40,7 @@
 
 namespace kvq {
 
-constexpr int kPdThreads = 13 * 32;
+constexpr int kPdThreads = 14 * 32;
 
 constexpr int pow2_at_least(int x) {
   int p = 32;
@@ -64,10 +63,10 @@ struct Pd {
   static constexpr int NCH = D == 256 ? 2 : 1;    // 128-byte columns of a token
   static constexpr int TPR = D == 64 ? 2 : 1;     // tokens of an smem row
   static constexpr int KT = 128 * TPR;            // tokens of a tile
-  static constexpr int NQS = 2 * R;               // N of the score MMA
+  static constexpr int NQS = max_of(16, 2 * R);   // N of the score MMA
   static constexpr int SBLK = TPR * NG;           // its column blocks
   // bytes of P of a token and group (3 R, to a swizzle width)
-  static constexpr int PW = R <= 4 ? 16 : (R <= 8 ? 32 : 64);
+  static constexpr int PW = R <= 4 && TPR == 2 ? 16 : (R <= 8 ? 32 : 64);
   static constexpr int NP = TPR * PW;             // N of the value MMA, for a group
   static constexpr int NGM = D == 256 ? max_of(1, NG / 2) : NG;  // P's of a 128-coordinate block
   static constexpr uint32_t PSW = NP == 32 ? kSw32 : (NP == 64 ? kSw64 : kSw128);
@@ -75,23 +74,27 @@ struct Pd {
   static constexpr int OBUF = 2 * SCOLS + 2 * OCOLS <= 256 ? 2 : 1;  // two blocks an SM
   static constexpr int TMEM = pow2_at_least(2 * SCOLS + OBUF * OCOLS);
   static_assert(TMEM <= 512, "tensor memory columns");
+  static constexpr int PBUF = NG >= 4 ? 1 : 2;    // P's in shared memory
   // shared memory, two of each
   static constexpr int TILE = NCH * 16384;        // expanded K or V
   static constexpr int QB = NCH * NQS * 128;
   static constexpr int PB = NG * 128 * NP;
   static constexpr int OB = TPR * R * D * 4;      // result of an item (one)
-  static constexpr int oK = 0, oV = 2 * TILE, oQ = 4 * TILE, oP = oQ + 2 * QB, oO = oP + 2 * PB;
-  static constexpr int SMEM = oO + OB + 1024;     // room to align the base
+  static constexpr int SC = KT * NG * 4;          // scales of K or V
+  static constexpr int oK = 0, oV = 2 * TILE, oQ = 4 * TILE, oP = oQ + 2 * QB,
+                       oO = oP + PBUF * PB;
+  static constexpr int oS = oO + OB;              // scales: K, V of one tile, then the other
+  static constexpr int SMEM = oS + 4 * SC + 1024;  // room to align the base
   static constexpr int KP = KT * (D / 32) / 128;  // 16-byte pieces of codes a thread
+  static constexpr int SP = (2 * SC / 16 + 127) / 128;  // and of scales
   // Blocks an SM: as many as registers, shared and tensor memory hold (the
   // occupancy calculator answers one for any kernel with tensor memory).
-  static constexpr int BLOCKS = R > 8 ? 1 : min_of(2, min_of(512 / TMEM, 230000 / (SMEM + 6144)));
-  static_assert(SMEM + 6144 <= 232448, "shared memory");
+  static constexpr int BLOCKS = R > 8 ? 1 : min_of(2, min_of(512 / TMEM, 233472 / (SMEM + 5120)));
+  static_assert(SMEM + 4096 <= 232448, "shared memory");
   static_assert(R % 4 == 0 && R <= 16 && NP >= 32, "rows");
 };
 
-// A tile as the control warp writes it down for the others, up to six tiles
-// ahead.
+// A tile as the page warp writes it down for the others, up to a ring ahead.
 struct PdTile {
   int t0, len;          // first token, cached rows of the sequence
   int c0, head, row0, rows;
@@ -99,10 +102,10 @@ struct PdTile {
   int whole, last;      // no row's limits lie inside; the item's last tile
   int64_t row[16];      // cache row of each 16 tokens, -1: not to be read
 };
-constexpr int kPdRing = 16;
+constexpr int kPdRing = 8;
 
 struct PdShared {
-  uint64_t dfull[kPdRing];                   // tile described
+  uint64_t dfull[kPdRing], dfree[kPdRing];   // tile described, description read
   uint64_t kfull[2], vfull[2], pfull[2], qfull[2];  // operands in shared memory
   uint64_t sdone[2], odone[2];               // MMAs done: S, or O, ready; operands free
   uint64_t sfree[2], ofree[2];               // S, O read
@@ -240,7 +243,10 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   if (tid == 0) {
-    for (int i = 0; i < kPdRing; ++i) mbar_init(bar(sh.dfull[i]), 1);
+    for (int i = 0; i < kPdRing; ++i) {
+      mbar_init(bar(sh.dfull[i]), 1);
+      mbar_init(bar(sh.dfree[i]), 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(sh.kfull[i]), 4);
       mbar_init(bar(sh.vfull[i]), 4);
@@ -276,28 +282,24 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     if (lane == 0) mbar_arrive(smem_u32(&b));
   };
 
-  if (warp == 12) {
-    // ---------------- control: descriptions, prefetches, MMAs ----------------
+  if (warp == 13) {
+    // ---------------- pages: what each tile is, and where ----------------
     Cursor<R, KT> c;
     c.seek(a, run.seq, run.off);
     if (lane == 0) sh.begun = run.begin - c.tile;
-    auto describe = [&](int i) {  // the cursor's tile as number i
+    for (int i = 0; i < n; ++i) {
       PdTile& e = sh.tiles[i % kPdRing];
+      if (i >= kPdRing) wait(sh.dfree[i % kPdRing], i / kPdRing - 1);
       const int t0 = (c.first + c.tile) * KT;
       int64_t r = -1;
       if (lane < KT / 16) {
         const int64_t t = int64_t(t0) + lane * 16;
         if (t < c.q.len) {
           const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
-          if (page < 0 || page >= a.n_pages) {
+          if (page < 0 || page >= a.n_pages)
             flag_bad_index(status);
-          } else {
+          else
             r = ((page * a.n_kv + c.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-            prefetch_l2(a.k_packed + r * (D / 2), 16 * (D / 2));
-            prefetch_l2(a.v_packed + r * (D / 2), 16 * (D / 2));
-            prefetch_l2(a.k_scales + r * NG, 64 * NG);
-            prefetch_l2(a.v_scales + r * NG, 64 * NG);
-          }
         }
         e.row[lane] = r;
       }
@@ -321,7 +323,9 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       }
       arrive(sh.dfull[i % kPdRing]);
       if (i + 1 < n && ++c.tile == c.count) c.next_item(a);
-    };
+    }
+  } else if (warp == 12) {
+    // ---------------- MMA issue ----------------
     auto scores = [&](int i, int item) {
       const uint32_t k = sbase + C::oK + (i & 1) * C::TILE;
       const uint32_t q = sbase + C::oQ + (item & 1) * C::QB;
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       mma_commit(bar(sh.sdone[i & 1]));
     };
     auto values = [&](int i) {
-      const uint32_t v = sbase + C::oV + (i & 1) * C::TILE, p = sbase + C::oP + (i & 1) * C::PB;
+      const uint32_t v = sbase + C::oV + (i & 1) * C::TILE, p = sbase + C::oP + (i % C::PBUF) * C::PB;
       // one MMA for all groups of a 128-coordinate block
       constexpr uint32_t id = instr_desc(kAccS32, kFmtS8, kFmtU8, true, true, 128, C::NGM * C::NP);
       tc_fence_after();
@@ -360,15 +364,15 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     };
     int item = 0;  // of the next tile whose scores are issued
     auto issue_scores = [&](int i) {
-      PdTile& e = sh.tiles[i % kPdRing];
-      if (i > 0 && e.starts) ++item;
-      if (e.starts) wait(sh.qfull[item & 1], item >> 1);
+      wait(sh.dfull[i % kPdRing], i / kPdRing);
+      const bool starts = sh.tiles[i % kPdRing].starts;
+      if (i > 0 && starts) ++item;
+      if (starts) wait(sh.qfull[item & 1], item >> 1);
       wait(sh.kfull[i & 1], i >> 1);
       if (i >= 2) wait(sh.sfree[i & 1], (i >> 1) - 1);
       if (lane == 0) scores(i, item);
       __syncwarp();
     };
-    for (int i = 0; i < min(6, n); ++i) describe(i);
     issue_scores(0);
     for (int i = 0; i < n; ++i) {
       if (i + 1 < n) issue_scores(i + 1);
@@ -377,12 +381,46 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       if (i >= C::OBUF) wait(sh.ofree[i % C::OBUF], (i / C::OBUF) - 1);
       if (lane == 0) values(i);
       __syncwarp();
-      if (i + 6 < n) describe(i + 6);
     }
   } else if (warp >= 8) {
     // ---------------- expansion: packed codes -> 16 c bytes ----------------
     const int et = tid - 256;
-    uint4 kreg[KP], vreg[KP];
+    uint4 kreg[KP], vreg[KP], sreg[C::SP];
+    // Into L2 what will be loaded in two tiles' time (a line a thread and step):
+    // the loads below are one tile ahead, which is less than a trip to memory.
+    auto prefetch = [&](int i) {
+      const PdTile& e = sh.tiles[i % kPdRing];
+      constexpr int LINES = KT * (D / 2) / 128;  // of K, and of V
+#pragma unroll
+      for (int k = 0; k < 2 * LINES / 128; ++k) {
+        const int p = (et + 128 * k) % LINES;
+        const uint8_t* base = et + 128 * k < LINES ? a.k_packed : a.v_packed;
+        const int64_t r = e.row[p * 256 / D >> 4];  // 256 / D rows a line
+        if (r >= 0)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(base + r * (D / 2) +
+                                                        (p * 128) % (16 * (D / 2))));
+      }
+    };
+    auto load_scales = [&](int i) {
+      const PdTile& e = sh.tiles[i % kPdRing];
+#pragma unroll
+      for (int k = 0; k < C::SP; ++k) {
+        const int p = et + 128 * k, q = p % (C::SC / 16);  // piece of K's, then of V's
+        sreg[k] = make_uint4(0, 0, 0, 0);
+        if (p < 2 * C::SC / 16) {
+          const int64_t r = e.row[q / (4 * NG)];
+          const float* base = p < C::SC / 16 ? a.k_scales : a.v_scales;
+          if (r >= 0)
+            sreg[k] = __ldg(reinterpret_cast<const uint4*>(base + r * NG) + q % (4 * NG));
+        }
+      }
+    };
+    auto store_scales = [&](uint32_t at) {
+#pragma unroll
+      for (int k = 0; k < C::SP; ++k)
+        if (et + 128 * k < 2 * C::SC / 16)
+          sts128(at + uint32_t(et + 128 * k) * 16, sreg[k].x, sreg[k].y, sreg[k].z, sreg[k].w);
+    };
     auto load = [&](int i, const uint8_t* base, uint4 (&w)[KP]) {
       const PdTile& e = sh.tiles[i % kPdRing];
 #pragma unroll
@@ -412,18 +450,28 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     wait(sh.dfull[0], 0);
     load(0, a.k_packed, kreg);
     load(0, a.v_packed, vreg);
+    load_scales(0);
+    for (int i = 1; i < min(3, n); ++i) {
+      wait(sh.dfull[i], 0);
+      prefetch(i);
+    }
     for (int i = 0; i < n; ++i) {
       if (i >= 2) wait(sh.sdone[i & 1], (i >> 1) - 1);
       expand(kreg, sbase + C::oK + (i & 1) * C::TILE);
       arrive(sh.kfull[i & 1]);
-      if (i + 1 < n) {
-        wait(sh.dfull[(i + 1) % kPdRing], (i + 1) / kPdRing);
-        load(i + 1, a.k_packed, kreg);
+      if (i + 1 < n) load(i + 1, a.k_packed, kreg);
+      if (i + 3 < n) {
+        wait(sh.dfull[(i + 3) % kPdRing], (i + 3) / kPdRing);
+        prefetch(i + 3);
       }
       if (i >= 2) wait(sh.odone[i & 1], (i >> 1) - 1);
+      store_scales(sbase + C::oS + (i & 1) * 2 * C::SC);
       expand(vreg, sbase + C::oV + (i & 1) * C::TILE);
       arrive(sh.vfull[i & 1]);
-      if (i + 1 < n) load(i + 1, a.v_packed, vreg);
+      if (i + 1 < n) {
+        load(i + 1, a.v_packed, vreg);
+        load_scales(i + 1);
+      }
     }
   } else if (warp < 4) {
     // ---------------- softmax: a token's scores -> weights ----------------
@@ -431,29 +479,12 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     constexpr int TPR = C::TPR;
     float m[R], l[R], cw[R];
     float ks[TPR][NG], vs[TPR][NG];
-    bool seen[TPR], fresh = true;
-    auto load_scales = [&](int i) {
-      const PdTile& e = sh.tiles[i % kPdRing];
-#pragma unroll
-      for (int h = 0; h < TPR; ++h) {
-        const int tl = row + 128 * h;
-        const int64_t r = e.row[tl >> 4];
-        seen[h] = r >= 0 && e.t0 + tl < e.len;
-#pragma unroll
-        for (int j = 0; j < NG; ++j) ks[h][j] = vs[h][j] = 0.0f;
-        if (seen[h]) {
-          const float* kp = a.k_scales + (r + (tl & 15)) * NG;
-          const float* vp = a.v_scales + (r + (tl & 15)) * NG;
-#pragma unroll
-          for (int j = 0; j < NG; ++j) ks[h][j] = __ldg(kp + j), vs[h][j] = __ldg(vp + j);
-        }
-      }
-    };
+    bool fresh = true;
     int item = -1;
-    wait(sh.dfull[0], 0);
-    load_scales(0);
     for (int i = 0; i < n; ++i) {
       const PdTile& e = sh.tiles[i % kPdRing];
+      wait(sh.vfull[i & 1], i >> 1);  // scales
+      wait(sh.dfull[i % kPdRing], i / kPdRing);
       const int rows = e.rows;
       if (e.starts) {
         ++item;
@@ -464,8 +495,17 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       }
       const float* qs = sh.qs[item & 1];
       float vmax[TPR];
+      bool seen[TPR];
 #pragma unroll
       for (int h = 0; h < TPR; ++h) {
+        const int tl = row + 128 * h;
+        const float* sc = reinterpret_cast<const float*>(smem + C::oS + (i & 1) * 2 * C::SC) + tl * NG;
+        seen[h] = e.whole || (e.t0 + tl < e.len && e.row[tl >> 4] >= 0);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {  // rows past the end may hold anything
+          ks[h][j] = seen[h] ? sc[j] : 0.0f;
+          vs[h][j] = seen[h] ? sc[C::SC / 4 + j] : 0.0f;
+        }
         vmax[h] = vs[h][0];
 #pragma unroll
         for (int j = 1; j < NG; ++j) vmax[h] = fmaxf(vmax[h], vs[h][j]);
@@ -509,8 +549,9 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
         }
       }
 
-      const uint32_t pt = sbase + C::oP + (i & 1) * C::PB;
-      if (i >= 2) wait(sh.odone[i & 1], (i >> 1) - 1);  // P is free
+      const uint32_t pt = sbase + C::oP + (i % C::PBUF) * C::PB;
+      if (i >= C::PBUF)  // P is free
+        wait(sh.odone[(i - C::PBUF) & 1], (i - C::PBUF) >> 1);
       auto weights = [&]() {
         bool over = false;
 #pragma unroll
@@ -617,10 +658,6 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
         }
       }
       arrive(sh.pfull[i & 1]);
-      if (i + 1 < n) {
-        wait(sh.dfull[(i + 1) % kPdRing], (i + 1) / kPdRing);
-        load_scales(i + 1);
-      }
     }
   } else {
     // ---------- accumulation, results, and the queries of the next items ----------
@@ -694,7 +731,10 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       }
       tc_fence_before();
       arrive(sh.ofree[i % C::OBUF]);
-      if (!e.ends) continue;
+      if (!e.ends) {
+        arrive(sh.dfree[i % kPdRing]);
+        continue;
+      }
 
       // ---- end of the item, or of the block's share of it ----
       const bool began_here = item > 0 || sh.begun == run.begin;
@@ -747,6 +787,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
         join->rows = rows;
         join->first_block = block_of(sh.begun, run.total, run.blocks);
       }
+      arrive(sh.dfree[i % kPdRing]);
       prepare_next(item + 2);
       ++item;
     }
