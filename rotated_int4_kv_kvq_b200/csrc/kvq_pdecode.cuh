@@ -100,13 +100,16 @@ struct PdTile {
   int c0, head, row0, rows;
   int starts, ends;     // first, last tile of its item (or of the block's share)
   int whole, last;      // no row's limits lie inside; the item's last tile
-  int64_t row[16];      // cache row of each 16 tokens, -1: not to be read
+  uint32_t have;        // bit i: tokens 16 i .. 16 i + 15 are there
+  int64_t row[16];      // cache row of each 16 tokens (0 where they are not)
 };
 constexpr int kPdRing = 8;
 
 struct PdShared {
   uint64_t dfull[kPdRing], dfree[kPdRing];   // tile described, description read
-  uint64_t kfull[2], vfull[2], pfull[2], qfull[2];  // operands in shared memory
+  uint64_t full[2], pfull[4], qfull[2];      // operands in shared memory: K and V, P, Q
+  // (Nobody may fall two phases behind a barrier it waits on.  The accumulation
+  // can be two tiles behind the softmax, hence pfull by four.)
   uint64_t sdone[2], odone[2];               // MMAs done: S, or O, ready; operands free
   uint64_t sfree[2], ofree[2];               // S, O read
   PdTile tiles[kPdRing];
@@ -211,6 +214,29 @@ __device__ __forceinline__ void pd_slices(const uint32_t* w, uint32_t& b0, uint3
   b2 = __byte_perm(__byte_perm(w[0], w[1], 0x0062), __byte_perm(w[2], w[3], 0x0062), 0x5410);
 }
 
+// As mbar_wait_bounded, for waits that are often long: the hardware may suspend
+// the warp for up to 2 us a poll (a role that waits costs few issue slots), and
+// the timer is read only after 64 of them.
+__device__ __forceinline__ bool mbar_wait_suspended(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0; it < KVQ_WAIT_MAX_POLLS; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(2000u)
+        : "memory");
+    if (done) return true;
+    if ((it & 63u) == 63u) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > KVQ_WAIT_LIMIT_NS) return false;
+    }
+  }
+  return false;
+}
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -248,9 +274,9 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       mbar_init(bar(sh.dfree[i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(sh.kfull[i]), 4);
-      mbar_init(bar(sh.vfull[i]), 4);
-      mbar_init(bar(sh.pfull[i]), 4);
+      mbar_init(bar(sh.full[i]), 4);
+      mbar_init(bar(sh.pfull[2 * i]), 4);
+      mbar_init(bar(sh.pfull[2 * i + 1]), 4);
       mbar_init(bar(sh.qfull[i]), 4);
       mbar_init(bar(sh.sdone[i]), 1);
       mbar_init(bar(sh.odone[i]), 1);
@@ -275,7 +301,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
   // A wait that runs out is recorded and skipped from then on: every role still
   // takes all its steps, so nobody is left at a barrier.
   auto wait = [&](uint64_t& b, int phase) {
-    if (ok) ok = mbar_wait_bounded(smem_u32(&b), uint32_t(phase) & 1u);
+    if (ok) ok = mbar_wait_suspended(smem_u32(&b), uint32_t(phase) & 1u);
   };
   auto arrive = [&](uint64_t& b) {  // one arrival for the warp
     __syncwarp();
@@ -291,24 +317,27 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       PdTile& e = sh.tiles[i % kPdRing];
       if (i >= kPdRing) wait(sh.dfree[i % kPdRing], i / kPdRing - 1);
       const int t0 = (c.first + c.tile) * KT;
-      int64_t r = -1;
+      int64_t r = 0;
+      bool there = false;
       if (lane < KT / 16) {
         const int64_t t = int64_t(t0) + lane * 16;
         if (t < c.q.len) {
           const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
-          if (page < 0 || page >= a.n_pages)
-            flag_bad_index(status);
-          else
+          there = page >= 0 && page < a.n_pages;
+          if (there)
             r = ((page * a.n_kv + c.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+          else
+            flag_bad_index(status);
         }
         e.row[lane] = r;
       }
-      const uint32_t have = __ballot_sync(kFull, r >= 0);
+      const uint32_t have = __ballot_sync(kFull, there);
       if (lane == 0) {
         const int row0 = c.qt * R;
         const int rows = int(min(int64_t(R), int64_t(c.q.n) * a.n_q - row0));
         const int pf = c.q.len - c.q.n + row0 / a.n_q;  // positions of the first and last row
         const int pl = c.q.len - c.q.n + (row0 + rows - 1) / a.n_q;
+        e.have = have;
         e.t0 = t0;
         e.len = c.q.len;
         e.c0 = c.q.c0;
@@ -368,7 +397,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       const bool starts = sh.tiles[i % kPdRing].starts;
       if (i > 0 && starts) ++item;
       if (starts) wait(sh.qfull[item & 1], item >> 1);
-      wait(sh.kfull[i & 1], i >> 1);
+      wait(sh.full[i & 1], i >> 1);
       if (i >= 2) wait(sh.sfree[i & 1], (i >> 1) - 1);
       if (lane == 0) scores(i, item);
       __syncwarp();
@@ -376,101 +405,87 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     issue_scores(0);
     for (int i = 0; i < n; ++i) {
       if (i + 1 < n) issue_scores(i + 1);
-      wait(sh.vfull[i & 1], i >> 1);
-      wait(sh.pfull[i & 1], i >> 1);
+      wait(sh.pfull[i & 3], i >> 2);
       if (i >= C::OBUF) wait(sh.ofree[i % C::OBUF], (i / C::OBUF) - 1);
       if (lane == 0) values(i);
       __syncwarp();
     }
   } else if (warp >= 8) {
     // ---------------- expansion: packed codes -> 16 c bytes ----------------
+    // Codes and scales are loaded right after the tile before is expanded: the
+    // proxy fence at the end of an expansion would wait for loads in flight.
+    // What hides their latency is the prefetch into L2 two tiles earlier.
     const int et = tid - 256;
     uint4 kreg[KP], vreg[KP], sreg[C::SP];
-    // Into L2 what will be loaded in two tiles' time (a line a thread and step):
-    // the loads below are one tile ahead, which is less than a trip to memory.
-    auto prefetch = [&](int i) {
+    const int piece = (et / (D / 32) & 15) * (D / 2) + et % (D / 32) * 16;  // in 16 tokens' codes
+    auto load = [&](int i) {
+      const PdTile& e = sh.tiles[i % kPdRing];
+#pragma unroll
+      for (int k = 0; k < KP; ++k) {
+        const int64_t off = e.row[(et + 128 * k) / (D / 2)] * (D / 2) + piece;
+        kreg[k] = __ldg(reinterpret_cast<const uint4*>(a.k_packed + off));
+        vreg[k] = __ldg(reinterpret_cast<const uint4*>(a.v_packed + off));
+      }
+#pragma unroll
+      for (int k = 0; k < C::SP; ++k) {
+        const int p = et + 128 * k, q = p % (C::SC / 16);  // piece of K's, then of V's
+        if (2 * C::SC / 16 >= 128 || p < 2 * C::SC / 16)
+          sreg[k] = __ldg(reinterpret_cast<const uint4*>(
+                              (p < C::SC / 16 ? a.k_scales : a.v_scales) +
+                              e.row[q / (4 * NG)] * NG) +
+                          q % (4 * NG));
+      }
+    };
+    auto prefetch = [&](int i) {  // a line a thread and step
       const PdTile& e = sh.tiles[i % kPdRing];
       constexpr int LINES = KT * (D / 2) / 128;  // of K, and of V
 #pragma unroll
       for (int k = 0; k < 2 * LINES / 128; ++k) {
         const int p = (et + 128 * k) % LINES;
         const uint8_t* base = et + 128 * k < LINES ? a.k_packed : a.v_packed;
-        const int64_t r = e.row[p * 256 / D >> 4];  // 256 / D rows a line
-        if (r >= 0)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(base + r * (D / 2) +
-                                                        (p * 128) % (16 * (D / 2))));
+        // 256 / D rows a line
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            base + e.row[p * 256 / D >> 4] * (D / 2) + (p * 128) % (16 * (D / 2))));
       }
     };
-    auto load_scales = [&](int i) {
-      const PdTile& e = sh.tiles[i % kPdRing];
-#pragma unroll
-      for (int k = 0; k < C::SP; ++k) {
-        const int p = et + 128 * k, q = p % (C::SC / 16);  // piece of K's, then of V's
-        sreg[k] = make_uint4(0, 0, 0, 0);
-        if (p < 2 * C::SC / 16) {
-          const int64_t r = e.row[q / (4 * NG)];
-          const float* base = p < C::SC / 16 ? a.k_scales : a.v_scales;
-          if (r >= 0)
-            sreg[k] = __ldg(reinterpret_cast<const uint4*>(base + r * NG) + q % (4 * NG));
-        }
-      }
-    };
-    auto store_scales = [&](uint32_t at) {
-#pragma unroll
-      for (int k = 0; k < C::SP; ++k)
-        if (et + 128 * k < 2 * C::SC / 16)
-          sts128(at + uint32_t(et + 128 * k) * 16, sreg[k].x, sreg[k].y, sreg[k].z, sreg[k].w);
-    };
-    auto load = [&](int i, const uint8_t* base, uint4 (&w)[KP]) {
-      const PdTile& e = sh.tiles[i % kPdRing];
-#pragma unroll
-      for (int k = 0; k < KP; ++k) {
-        const int p = et + 128 * k, t = p / (D / 32);
-        const int64_t r = e.row[t >> 4];
-        w[k] = make_uint4(0, 0, 0, 0);
-        if (r >= 0)
-          w[k] = __ldg(reinterpret_cast<const uint4*>(base + r * (D / 2)) +
-                       (t & 15) * (D / 32) + p % (D / 32));
-      }
-    };
+    // Where this thread's pieces go: rows 128 / (D / 32) apart for each k, the
+    // same column (at d = 64 the other half from the middle on).
+    const int r0 = et / (D / 32), col = et % (D / 32) * 32;
+    const uint32_t dst0 = uint32_t(col >> 7) * 16384 + uint32_t(r0) * 128 +
+                          (((uint32_t(col & 127) >> 4) ^ uint32_t(r0 & 7)) * 16);
     auto expand = [&](const uint4 (&w)[KP], uint32_t tile) {
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
-        const int p = et + 128 * k, t = p / (D / 32);
-        const int r = t & 127;
-        const int byte = (t >> 7) * 64 + p % (D / 32) * 32;  // in the row's bytes
-        const uint32_t base = tile + uint32_t(byte >> 7) * 16384 + uint32_t(r) * 128;
-        const uint32_t c0 = (uint32_t(byte & 127) >> 4) ^ uint32_t(r & 7), c1 = c0 ^ 1u;
         constexpr uint32_t H = 0xF0F0F0F0u;
-        sts128(base + c0 * 16, (w[k].x << 4) & H, w[k].x & H, (w[k].y << 4) & H, w[k].y & H);
-        sts128(base + c1 * 16, (w[k].z << 4) & H, w[k].z & H, (w[k].w << 4) & H, w[k].w & H);
+        const int down = k * (4096 / D) % 128;  // rows
+        const bool other = C::TPR == 2 && k * (4096 / D) >= 128;
+        const uint32_t at = tile + (other ? dst0 ^ 64u : dst0) + down * 128;
+        sts128(at, (w[k].x << 4) & H, w[k].x & H, (w[k].y << 4) & H, w[k].y & H);
+        sts128(at ^ 16u, (w[k].z << 4) & H, w[k].z & H, (w[k].w << 4) & H, w[k].w & H);
       }
-      fence_proxy_async_smem();
     };
     wait(sh.dfull[0], 0);
-    load(0, a.k_packed, kreg);
-    load(0, a.v_packed, vreg);
-    load_scales(0);
+    load(0);
     for (int i = 1; i < min(3, n); ++i) {
       wait(sh.dfull[i], 0);
       prefetch(i);
     }
     for (int i = 0; i < n; ++i) {
-      if (i >= 2) wait(sh.sdone[i & 1], (i >> 1) - 1);
-      expand(kreg, sbase + C::oK + (i & 1) * C::TILE);
-      arrive(sh.kfull[i & 1]);
-      if (i + 1 < n) load(i + 1, a.k_packed, kreg);
+      const int buf = i & 1;
+      if (i >= 2) wait(sh.odone[buf], (i >> 1) - 1);  // K, V, P and scales are free
+      expand(kreg, sbase + C::oK + buf * C::TILE);
+      expand(vreg, sbase + C::oV + buf * C::TILE);
+#pragma unroll
+      for (int k = 0; k < C::SP; ++k)
+        if (2 * C::SC / 16 >= 128 || et + 128 * k < 2 * C::SC / 16)
+          sts128(sbase + C::oS + buf * 2 * C::SC + uint32_t(et + 128 * k) * 16, sreg[k].x,
+                 sreg[k].y, sreg[k].z, sreg[k].w);
+      fence_proxy_async_smem();
+      arrive(sh.full[buf]);
+      if (i + 1 < n) load(i + 1);
       if (i + 3 < n) {
         wait(sh.dfull[(i + 3) % kPdRing], (i + 3) / kPdRing);
         prefetch(i + 3);
-      }
-      if (i >= 2) wait(sh.odone[i & 1], (i >> 1) - 1);
-      store_scales(sbase + C::oS + (i & 1) * 2 * C::SC);
-      expand(vreg, sbase + C::oV + (i & 1) * C::TILE);
-      arrive(sh.vfull[i & 1]);
-      if (i + 1 < n) {
-        load(i + 1, a.v_packed, vreg);
-        load_scales(i + 1);
       }
     }
   } else if (warp < 4) {
@@ -483,8 +498,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     int item = -1;
     for (int i = 0; i < n; ++i) {
       const PdTile& e = sh.tiles[i % kPdRing];
-      wait(sh.vfull[i & 1], i >> 1);  // scales
-      wait(sh.dfull[i % kPdRing], i / kPdRing);
+      wait(sh.full[i & 1], i >> 1);  // scales, and the description
       const int rows = e.rows;
       if (e.starts) {
         ++item;
@@ -500,7 +514,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       for (int h = 0; h < TPR; ++h) {
         const int tl = row + 128 * h;
         const float* sc = reinterpret_cast<const float*>(smem + C::oS + (i & 1) * 2 * C::SC) + tl * NG;
-        seen[h] = e.whole || (e.t0 + tl < e.len && e.row[tl >> 4] >= 0);
+        seen[h] = e.whole || (e.t0 + tl < e.len && (e.have >> (tl >> 4) & 1u));
 #pragma unroll
         for (int j = 0; j < NG; ++j) {  // rows past the end may hold anything
           ks[h][j] = seen[h] ? sc[j] : 0.0f;
@@ -595,51 +609,53 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       float lold[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) lold[r] = l[r];
-      const bool over = fresh ? true : weights();
-      const bool slow = named_or(1, 128, over);
-      if (slow) {
-        // the tile's maxima -> new references; then the weights once more
+      bool slow = fresh;
+      for (;;) {
+        if (slow) {  // the tile's maxima -> new references
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          l[r] = lold[r];
-          float x = -INFINITY;
+          for (int r = 0; r < R; ++r) {
+            l[r] = lold[r];
+            float x = -INFINITY;
 #pragma unroll
-          for (int h = 0; h < TPR; ++h) x = fmaxf(x, s[h][r]);
-          if (r >= rows) x = -INFINITY;
+            for (int h = 0; h < TPR; ++h) x = fmaxf(x, s[h][r]);
+            if (r >= rows) x = -INFINITY;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-          if (lane == 0) sh.red[warp][r] = x;
+            for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+            if (lane == 0) sh.red[warp][r] = x;
+          }
+          named_sync(1, 128);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float mn = m[r];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mn = fmaxf(mn, sh.red[w][r]);
+            const float f = ex2(m[r] - mn);
+            l[r] *= f;
+            m[r] = mn;
+            float x = 0.0f;
+#pragma unroll
+            for (int h = 0; h < TPR; ++h)
+              if (r < rows) x = fmaxf(x, ex2(s[h][r] - mn) * vmax[h]);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+            if (lane == 0) sh.red2[warp][r] = x;
+            if (row == 0) sh.fcur[r] = f, sh.mcur[r] = mn;
+          }
+          named_sync(1, 128);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float x = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.red2[w][r]);
+            // the power of two that brings the largest into [1/2, 1)
+            const int ex = min(max(253 - int(__float_as_uint(x) >> 23), 1), 237);
+            cw[r] = __uint_as_float(uint32_t(ex) << 23);
+            if (row == 0) sh.icwcur[r] = __uint_as_float(uint32_t(254 - ex) << 23);
+          }
         }
-        named_sync(1, 128);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float mn = m[r];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) mn = fmaxf(mn, sh.red[w][r]);
-          const float f = ex2(m[r] - mn);
-          l[r] *= f;
-          m[r] = mn;
-          float x = 0.0f;
-#pragma unroll
-          for (int h = 0; h < TPR; ++h)
-            if (r < rows) x = fmaxf(x, ex2(s[h][r] - mn) * vmax[h]);
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-          if (lane == 0) sh.red2[warp][r] = x;
-          if (row == 0) sh.fcur[r] = f, sh.mcur[r] = mn;
-        }
-        named_sync(1, 128);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float x = 0.0f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.red2[w][r]);
-          // the power of two that brings the largest into [1/2, 1)
-          const int ex = min(max(253 - int(__float_as_uint(x) >> 23), 1), 237);
-          cw[r] = __uint_as_float(uint32_t(ex) << 23);
-          if (row == 0) sh.icwcur[r] = __uint_as_float(uint32_t(254 - ex) << 23);
-        }
-        weights();
+        const bool over = weights();
+        if (slow || !named_or(1, 128, over)) break;
+        slow = true;
       }
       fresh = false;
       __syncwarp();
@@ -657,7 +673,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
           if (lane == 0) sh.l[i & 3][warp][r] = x;
         }
       }
-      arrive(sh.pfull[i & 1]);
+      arrive(sh.pfull[i & 3]);
     }
   } else {
     // ---------- accumulation, results, and the queries of the next items ----------
@@ -695,7 +711,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     int item = 0;
     float acc[C::NCH][R];
     for (int i = 0; i < n; ++i) {
-      wait(sh.dfull[i % kPdRing], i / kPdRing);
+      wait(sh.pfull[i & 3], i >> 2);  // the softmax's words on this tile
       const PdTile& e = sh.tiles[i % kPdRing];
       if (e.starts) {
 #pragma unroll

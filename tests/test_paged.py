@@ -495,6 +495,60 @@ def test_attend_empty_and_bad(kvq, news):
     assert st == 11 and (out[:news[0]] == 0).all() and torch.equal(out[news[0]:], good[news[0]:])
 
 
+def attend_f64(q, cache, cu, lens, table, window=0):
+    """O.attend_paged on the GPU, for sizes the oracle is too slow for: its own
+    rotation matrix, float64 throughout."""
+    R = torch.from_numpy(O.rotation_matrix(cache.d, cache.rot)).cuda()
+    R = R * cache.signs.double()
+    nq = q.shape[1] // cache.n_kv_heads
+    out = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+
+    def values(packed, scales, pages, n):
+        p = packed[pages].transpose(0, 1).flatten(1, 2)[:, :n].to(torch.int16)
+        c = torch.stack([p & 15, p >> 4], -1).flatten(-2)
+        c = torch.where(c > 7, c - 16, c).double()
+        s = scales[pages].transpose(0, 1).flatten(1, 2)[:, :n].double()
+        return (c * s.repeat_interleave(cache.group, -1)) @ R
+    for s, n in enumerate(lens):
+        pages = table[s, :-(-n // cache.page_size)].long()
+        k = values(cache.k_packed, cache.k_scales, pages, n)
+        v = values(cache.v_packed, cache.v_scales, pages, n)
+        m = cu[s + 1] - cu[s]
+        at = n - m + torch.arange(m, device="cuda")[:, None]
+        t = torch.arange(n, device="cuda")
+        hide = (t > at) | ((t <= at - window) if window else torch.zeros_like(t > at))
+        for h in range(cache.n_kv_heads):
+            x = q[cu[s]:cu[s + 1], h * nq:(h + 1) * nq].double().transpose(0, 1)
+            w = (x @ k[h].T * cache.d ** -0.5).masked_fill(hide, -torch.inf).softmax(-1)
+            out[cu[s]:cu[s + 1], h * nq:(h + 1) * nq] = (w @ v[h]).transpose(0, 1)
+    return out
+
+
+def check_large(kvq, cache, q, cu, lens, table, window=0, limit=None):
+    """By the 2-norm of each row: rounding alone leaves about u / sqrt(3) of it,
+    scores from 11-bit queries and weights of 11 bits as much again for scores
+    of a few units; 4 u bounds the three.  A limit of a case replaces it."""
+    dev = dict(device="cuda", dtype=torch.int32)
+    got = kvq.kvq_paged_attend(q, cache, torch.tensor(cu, **dev), torch.tensor(lens, **dev), table,
+                               max_q_len=max(b - a for a, b in zip(cu, cu[1:])), window=window)
+    assert kvq.kvq_device_status() == 0
+    ref = attend_f64(q, cache, cu, lens, table, window)
+    err = (got.double() - ref).norm(dim=-1) / ref.norm(dim=-1)
+    assert err.max().item() <= (4 * UNIT[q.dtype] if limit is None else limit)
+
+
+@pytest.mark.parametrize("d,group,nq,heads,page,seqs,length", [
+    (64, 64, 1, 32, 16, 10, 16000), (64, 32, 3, 32, 64, 6, 9000), (128, 32, 4, 16, 32, 12, 8000),
+    (128, 128, 8, 16, 16, 10, 6000), (256, 256, 4, 16, 64, 8, 5000), (256, 32, 8, 8, 16, 8, 5000)])
+def test_attend_one_token_long(kvq, d, group, nq, heads, page, seqs, length):
+    """Runs of many tiles and of several items in every block."""
+    lens = [max(1, length * (s + 1) // seqs - s) for s in range(seqs)]
+    cache = make_pool(kvq, d, sum(-(-m // page) for m in lens), heads, page, d, group, 0)
+    table = make_batch(cache, 17, lens)
+    q = rows(gen(18), seqs, heads * nq, d, torch.float16) * 0.25
+    check_large(kvq, cache, q, list(range(seqs + 1)), lens, table)
+
+
 def test_attend_many_sequences(kvq):
     """More sequences than threads of a block, most of them idle."""
     n = 1500
