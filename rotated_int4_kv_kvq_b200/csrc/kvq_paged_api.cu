@@ -167,7 +167,7 @@ int64_t kvq_paged_attend_workspace(int64_t n_tokens, int32_t n_kv_heads, int32_t
   if (n_tokens < 0 || n_tokens > kMaxRows || n_kv_heads < 1 || n_q < 1 || n_q > 64 ||
       int64_t(n_kv_heads) * n_q > 65535 || n_tokens * n_kv_heads * n_q > kMaxRows || max_q_len < 1)
     return -KVQ_ERR_BAD_SIZE;
-  return kvq::few_rows_workspace(d);
+  return kvq::attn_workspace(d, int64_t(max_q_len) * n_q);
 }
 
 kvq_status kvq_paged_attend(const void* q, kvq_dtype dtype, int64_t n_tokens, int64_t q_stride,

@@ -8,6 +8,7 @@
 #include <utility>
 
 #include "kvq_paged.cuh"
+#include "kvq_pchunk.cuh"
 #include "kvq_pdecode.cuh"
 #include "kvq_paged_launch.h"
 
@@ -116,6 +117,42 @@ cudaError_t few_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t strea
              : launch_paged(kvq_paged_join_kernel<D, R, kRotSRHT>, grid, 256, 0, stream, a);
 }
 
+template <int D, int NG>
+cudaError_t many_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t stream, unsigned* st) {
+  using C = Pc<D, NG>;
+  constexpr auto kern = kvq_paged_chunk_kernel<D, NG>;
+  cudaError_t e = paged_setup<kern>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (args.n_tokens * args.n_q + C::M - 1) / C::M + args.n_seqs;
+  const int64_t tiles = (args.max_pages << args.page_shift) / C::KT + 1;
+  int64_t grid = std::min<int64_t>(sm_count, kMaxChunkBlocks);
+  if (items * args.n_kv < grid)
+    grid = std::min<int64_t>(grid, items * args.n_kv * std::min<int64_t>(tiles, grid));
+  PagedAttnArgs a = args;
+  a.join = reinterpret_cast<JoinInfo*>(a.workspace);
+  a.parts = reinterpret_cast<float*>(a.workspace + kMaxBlocks * 32);
+  e = launch_paged(kern, grid, C::THREADS, C::SMEM, stream, a, st);
+  if (e != cudaSuccess) return e;
+  return a.rot == kRotSRFT
+             ? launch_paged(kvq_paged_join_kernel<D, C::M, kRotSRFT>, grid, 256, 0, stream, a)
+             : launch_paged(kvq_paged_join_kernel<D, C::M, kRotSRHT>, grid, 256, 0, stream, a);
+}
+
+template <int D>
+cudaError_t many_rows_group(const PagedAttnArgs& a, int sm_count, cudaStream_t stream,
+                            unsigned* st) {
+  switch (D / a.group) {
+    case 1: return many_rows<D, 1>(a, sm_count, stream, st);
+    case 2: return many_rows<D, 2>(a, sm_count, stream, st);
+    case 4:
+      if constexpr (D >= 128) return many_rows<D, 4>(a, sm_count, stream, st);
+      break;
+    case 8:
+      if constexpr (D >= 256) return many_rows<D, 8>(a, sm_count, stream, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
 template <int D, int R>
 cudaError_t few_rows_group(const PagedAttnArgs& a, int sm_count, cudaStream_t stream,
                            unsigned* st) {
@@ -173,6 +210,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int max_q_len, int sm_coun
   unsigned* st;
   cudaError_t e = detail::paged_status_ptr(&st);
   if (e != cudaSuccess) return e;
+  if (int64_t(max_q_len) * a.n_q > kFewRows)
+    return detail::many_rows_group<D>(a, sm_count, stream, st);
   const int r = few_rows_item(D, a.group, int64_t(max_q_len) * a.n_q);
   if (r == 4) return detail::few_rows_group<D, 4>(a, sm_count, stream, st);
   return r == 8 ? detail::few_rows_group<D, 8>(a, sm_count, stream, st)

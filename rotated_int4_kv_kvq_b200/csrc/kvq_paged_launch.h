@@ -73,8 +73,13 @@ constexpr int few_rows_item(int d, int group, int64_t rows) {
   return rows <= 4 ? 4 : (rows <= 8 || (d == 256 && group <= 64) ? 8 : 16);
 }
 constexpr int64_t kMaxBlocks = 148 * 4;  // of the few-rows kernel
-constexpr int64_t few_rows_workspace(int d) {
-  return kMaxBlocks * 32 + kMaxBlocks * 2 * 16 * (int64_t(d) + 2) * 4;
+constexpr int64_t kMaxChunkBlocks = 148;  // of the many-rows kernel, one an SM
+// Up to this many rows of a sequence and KV head the few-rows kernel runs.
+constexpr int64_t kFewRows = 16;
+constexpr int64_t attn_workspace(int d, int64_t rows) {
+  const int64_t slots = rows <= kFewRows ? kMaxBlocks * 2 * 16
+                                         : kMaxChunkBlocks * 2 * (d == 256 ? 128 : 256);
+  return kMaxBlocks * 32 + slots * (int64_t(d) + 2) * 4;
 }
 
 // Implemented once per d in the matching translation unit.

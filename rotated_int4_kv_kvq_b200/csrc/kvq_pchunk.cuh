@@ -1,0 +1,640 @@
+// kvq_pchunk.cuh -- attention of many query rows (a chunk of a prompt) over the
+// paged int4 cache.
+//
+// Mathematics as in kvq_pdecode.cuh: queries are rotated once, products run on
+// the codes in the rotated domain, results are rotated back once.  Here the
+// query rows are the large operand and the work is bound by the tensor cores
+// (4 d flops a row and key) and by the 2^x of every score.
+//
+//   S = Q C_K^T      kind::f16, f32 accumulators: Q the rotated queries in fp16
+//                    (each row scaled by a power of two, error 2^-12 of a
+//                    value: as much as rounding a query to fp16 once), C_K the
+//                    codes, exact
+//   p = 2^(S s_K[t] c_row - m)      f32; the row's reference m moves only when
+//                    its maximum exceeds it by 8, so the accumulators are
+//                    rescaled rarely
+//   O += P C_V       P = p s_V[t] 2^-v in fp16 (error 2^-12 of a weight, as in
+//                    any fp16 product), v a power of two that the V scales
+//                    seen so far stay under
+// With several scales a row (g < d) a row's largest scale is kept apart in f32
+// and the codes are multiplied by the ratios s_j / s_max, rounded to fp16.
+//
+// A block holds 256 query rows (two tiles of 128; one at d = 256, where tensor
+// memory holds one): while the tensor cores work for one tile the other one's
+// scores become weights.  Roles: four warps of softmax a tile (a thread a row;
+// they also rotate their rows in and out), four that turn packed codes into
+// fp16 operands (a thread a token), one that issues MMAs, one that looks pages
+// up.  P overwrites S in tensor memory and is read from there.
+#pragma once
+
+#include "kvq_pdecode.cuh"
+
+namespace kvq {
+
+template <int D_, int NG_>
+struct Pc {
+  static constexpr int D = D_, NG = NG_, G = D / NG;
+  static constexpr int NT = D == 256 ? 1 : 2;   // row tiles of a block
+  static constexpr int M = 128 * NT;            // query rows of an item
+  static constexpr int KT = 128;                // tokens of a tile
+  static constexpr int KS = D == 256 ? 1 : 2;   // K and V operands in shared memory
+  static constexpr int SLOTS = 2;               // S/P areas: a row tile each, or alternating
+  static constexpr int NCH = D / 64;            // 128-byte columns of a row
+  static constexpr int TILE = NCH * 16384;      // Q tile, K or V: 128 rows
+  static constexpr int oQ = 0, oK = NT * TILE, oV = oK + KS * TILE;
+  static constexpr int SMEM = oV + KS * TILE + 1024;
+  static constexpr int WARPS = NT * 4 + 6;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int W_DEQ = NT * 4, W_MMA = W_DEQ + 4, W_PAGE = W_MMA + 1;
+  static constexpr uint32_t colO = 256;         // tensor memory: S/P slots, then O
+  static_assert(SMEM + 4096 <= 232448, "shared memory");
+};
+
+struct PcTile {
+  int t0, len, c0, head, row0, rows, p0;
+  int starts, last, ends;
+  uint32_t have;
+  int64_t row[8];
+};
+constexpr int kPcRing = 8;
+
+struct PcShared {
+  uint64_t dfull[kPcRing], dfree[kPcRing];
+  uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
+  uint64_t scfull[4];            // scales
+  uint64_t qfull[2], sdone[2], pfull[2], odone[2];
+  PcTile tiles[kPcRing];
+  uint32_t tmem;
+  int64_t begun;
+  float ks[4][128], vs[4][128];  // by tile: K scales; V scales over 2^vexp
+  int vexp[4];
+  float wmax[2][4];
+  int64_t scratch[16 + 4];
+};
+
+// fp16 pairs of eight codes in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 codes_to_half(uint32_t w) {
+  const uint32_t w8 = w >> 8;
+  const __half2 b = __half2half2(__float2half(-1032.0f)), s = __half2half2(__float2half(0.0625f)),
+                c = __half2half2(__float2half(-72.0f));
+  auto h = [](uint32_t x) { return *reinterpret_cast<__half2*>(&x); };
+  auto u = [](__half2 x) { return *reinterpret_cast<uint32_t*>(&x); };
+  return make_uint4(u(__hadd2(h((w & 0x000F000Fu) ^ 0x64086408u), b)),
+                    u(__hfma2(h((w & 0x00F000F0u) ^ 0x64806480u), s, c)),
+                    u(__hadd2(h((w8 & 0x000F000Fu) ^ 0x64086408u), b)),
+                    u(__hfma2(h((w8 & 0x00F000F0u) ^ 0x64806480u), s, c)));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// Column of coordinate i in that order.
+__device__ __forceinline__ constexpr int pc_col(int i) {
+  return (i & ~7) | ((i & 3) << 1) | ((i >> 2) & 1);
+}
+
+// D (+)= A B with A (fp16) in tensor memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+      : "memory");
+}
+#define KVQ_V4(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+#define KVQ_V16(i) KVQ_V4(i), KVQ_V4(i + 4), KVQ_V4(i + 8), KVQ_V4(i + 12)
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15};" ::KVQ_V16(0),
+      "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31};" ::KVQ_V16(0),
+      KVQ_V16(16), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Rotates one query row into the Q tile; returns (in every lane) the factor
+// from its products to log2 scores.
+template <int D, int ROT>
+__device__ __forceinline__ float pc_query(const PagedAttnArgs& a, const uint16_t* src, uint32_t tile,
+                                          int r, const WideLane<D, ROT>& L) {
+  using P = Wide<D, ROT>;
+  f2 z[P::C];
+#pragma unroll
+  for (int j = 0; j < P::C; ++j) {
+    const int w = ROT == kRotSRFT ? L.lane + 32 * j : P::C * L.lane + j;
+    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(src) + w) ^ L.mask[j];
+    const float2 f = a.dtype == kDtF16 ? pair_to_float2<kDtF16>(v) : pair_to_float2<kDtBF16>(v);
+    z[j] = mk2(f.x, f.y);
+  }
+  float Y[P::W];
+  wide_rotate_fwd<D, ROT>(z, L, Y);
+  float top = 0.0f;
+#pragma unroll
+  for (int w = 0; w < P::W; ++w) top = fmaxf(top, fabsf(Y[w]));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+  // largest value into [2^8, 2^9): far from fp16's smallest and largest
+  const int e = min(max(int(__float_as_uint(top) >> 23), 20), 234);
+  const float mul = __uint_as_float(uint32_t(262 - e) << 23);   // 2^(135 - e)
+  const float back = __uint_as_float(uint32_t(e - 8) << 23);    // its inverse
+  const float sg = a.qscale < 0.0f ? -mul : mul;
+#pragma unroll
+  for (int w = 0; w < P::W; ++w) {
+    const int c = pc_col(L.k2 * P::W + w);
+    const uint32_t at = tile + uint32_t(c >> 6) * 16384 + uint32_t(r) * 128 +
+                        ((uint32_t(c & 63) * 2) ^ (uint32_t(r & 7) << 4));
+    const __half h = __float2half_rn(Y[w] * sg);
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const uint16_t*>(&h))
+                 : "memory");
+  }
+  return back * P::KAPPA * fabsf(a.qscale);
+}
+
+template <int D, int NG>
+__global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
+    kvq_paged_chunk_kernel(const PagedAttnArgs a, unsigned* status) {
+  using C = Pc<D, NG>;
+  constexpr int NT = C::NT, M = C::M, KT = C::KT, KS = C::KS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PcShared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  if (tid == 0) {
+    for (int i = 0; i < kPcRing; ++i) {
+      mbar_init(bar(sh.dfull[i]), 1);
+      mbar_init(bar(sh.dfree[i]), NT * 4);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(bar(sh.scfull[i]), 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(sh.kfull[i]), 4);
+      mbar_init(bar(sh.vfull[i]), 4);
+      mbar_init(bar(sh.kfree[i]), 1);
+      mbar_init(bar(sh.vfree[i]), 1);
+      mbar_init(bar(sh.qfull[i]), 4);
+      mbar_init(bar(sh.pfull[i]), 4);
+      mbar_init(bar(sh.sdone[i]), 1);
+      mbar_init(bar(sh.odone[i]), 1);
+    }
+    fence_mbar_init();
+  }
+  pdl_wait();  // no global access before the previous kernel completes
+  const Run run = find_run<M, KT, C::THREADS>(a, blockIdx.x, gridDim.x, sh.scratch, status);
+  JoinInfo* join = a.join + blockIdx.x;
+  if (tid == 0) join->first_block = -1;
+  if (run.begin == run.end) return;
+  const int n = int(run.end - run.begin);  // tiles
+  if (warp == C::W_MMA) tmem_alloc(smem_u32(&sh.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  bool ok = true;
+  // A wait that runs out is recorded and skipped from then on: every role still
+  // takes all its steps, so nobody is left at a barrier.
+  auto wait = [&](uint64_t& b, int phase) {
+    if (ok) ok = mbar_wait_suspended(smem_u32(&b), uint32_t(phase) & 1u);
+  };
+  auto arrive = [&](uint64_t& b) {  // one arrival for the warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&b));
+  };
+
+  if (warp == C::W_PAGE) {
+    // ---------------- pages: what each tile is, and where ----------------
+    Cursor<M, KT> c;
+    c.seek(a, run.seq, run.off);
+    if (lane == 0) sh.begun = run.begin - c.tile;
+    for (int i = 0; i < n; ++i) {
+      PcTile& e = sh.tiles[i % kPcRing];
+      if (i >= kPcRing) wait(sh.dfree[i % kPcRing], i / kPcRing - 1);
+      const int t0 = (c.first + c.tile) * KT;
+      int64_t r = 0;
+      bool there = false;
+      if (lane < KT / 16) {
+        const int64_t t = int64_t(t0) + lane * 16;
+        if (t < c.q.len) {
+          const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
+          there = page >= 0 && page < a.n_pages;
+          if (there)
+            r = ((page * a.n_kv + c.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+          else
+            flag_bad_index(status);
+        }
+        e.row[lane] = r;
+      }
+      const uint32_t have = __ballot_sync(kFull, there);
+      if (lane == 0) {
+        e.t0 = t0;
+        e.len = c.q.len;
+        e.c0 = c.q.c0;
+        e.head = c.head;
+        e.row0 = c.qt * M;
+        e.rows = int(min(int64_t(M), int64_t(c.q.n) * a.n_q - int64_t(c.qt) * M));
+        e.p0 = c.q.len - c.q.n;
+        e.starts = i == 0 || c.tile == 0;
+        e.last = c.tile + 1 == c.count;
+        e.ends = e.last || i + 1 == n;
+        e.have = have;
+      }
+      arrive(sh.dfull[i % kPcRing]);
+      if (i + 1 < n && ++c.tile == c.count) c.next_item(a);
+    }
+  } else if (warp == C::W_MMA) {
+    // ---------------- MMA issue ----------------
+    constexpr uint32_t idS = instr_desc(kAccF32, kFmtF16, kFmtF16, false, false, 128, KT);
+    constexpr uint32_t idO = instr_desc(kAccF32, kFmtF16, kFmtF16, false, true, 128, D);
+    int items[2] = {0, 0}, used[2] = {0, 0};  // of each row tile: items and tiles it took part in
+    bool two = false;
+    auto scores = [&](int x, int i) {  // row tile x, tile i
+      const int slot = NT == 2 ? x : i & 1;
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t q = sbase + C::oQ + x * C::TILE, k = sbase + C::oK + (i % KS) * C::TILE;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          mma_f16(tmem + slot * 128, smem_desc(q + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128),
+                  smem_desc(k + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128), idS, s > 0);
+        mma_commit(bar(sh.sdone[slot]));
+        if (x == NT - 1 || !two) mma_commit(bar(sh.kfree[i % KS]));
+      }
+      __syncwarp();
+    };
+    auto values = [&](int x, int i, bool first) {
+      const int slot = NT == 2 ? x : i & 1;
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t v = sbase + C::oV + (i % KS) * C::TILE;
+#pragma unroll
+        for (int s = 0; s < KT / 16; ++s)
+          mma_f16_ts(tmem + C::colO + x * 128, tmem + slot * 128 + s * 8,
+                     smem_desc(v + s * 2048, 16384, 1024, kSw128), idO, !first || s > 0);
+        mma_commit(bar(sh.odone[x]));
+        if (x == NT - 1 || !two) mma_commit(bar(sh.vfree[i % KS]));
+      }
+      __syncwarp();
+    };
+    for (int i = 0; i < n; ++i) {
+      wait(sh.dfull[i % kPcRing], i / kPcRing);
+      const bool starts = sh.tiles[i % kPcRing].starts, ends = sh.tiles[i % kPcRing].ends;
+      if (starts) {
+        two = NT == 2 && sh.tiles[i % kPcRing].rows > 128;
+        wait(sh.qfull[0], items[0]++);
+        if (two) wait(sh.qfull[1], items[1]++);
+        wait(sh.kfull[i % KS], i / KS);
+        scores(0, i);
+        if (two) scores(1, i);
+      }
+      if constexpr (NT == 2) {
+        wait(sh.pfull[0], used[0]++);
+        wait(sh.vfull[i % KS], i / KS);
+        values(0, i, starts);
+        if (!ends) {
+          wait(sh.kfull[(i + 1) % KS], (i + 1) / KS);
+          scores(0, i + 1);
+        }
+        if (two) {
+          wait(sh.pfull[1], used[1]++);
+          values(1, i, starts);
+          if (!ends) scores(1, i + 1);
+        }
+      } else {
+        if (!ends) {
+          wait(sh.kfull[(i + 1) % KS], (i + 1) / KS);
+          scores(0, i + 1);
+        }
+        wait(sh.pfull[i & 1], i >> 1);
+        wait(sh.vfull[i % KS], i / KS);
+        values(0, i, starts);
+      }
+    }
+  } else if (warp >= C::W_DEQ) {
+    // ---------------- packed codes -> fp16 operands, a thread a token ----------------
+    const int t = tid - C::W_DEQ * 32;
+    constexpr int NP = D / 32;  // 16-byte pieces of a row
+    uint4 kreg[NP], vreg[NP];
+    float ksc[NG], vsc[NG];
+    auto load = [&](int i) {
+      const PcTile& e = sh.tiles[i % kPcRing];
+      const int64_t r = e.row[t >> 4] + (t & 15);
+      const uint4* kp = reinterpret_cast<const uint4*>(a.k_packed + r * (D / 2));
+      const uint4* vp = reinterpret_cast<const uint4*>(a.v_packed + r * (D / 2));
+      const bool there = (e.have >> (t >> 4) & 1u) && e.t0 + t < e.len;
+#pragma unroll
+      for (int k = 0; k < NP; ++k) kreg[k] = __ldg(kp + k), vreg[k] = __ldg(vp + k);
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {  // rows past the end may hold anything
+        ksc[j] = there ? __ldg(a.k_scales + r * NG + j) : 0.0f;
+        vsc[j] = there ? __ldg(a.v_scales + r * NG + j) : 0.0f;
+      }
+    };
+    auto convert = [&](const uint4 (&w)[NP], const float (&sc)[NG], float top, uint32_t tile) {
+      const float inv = top > 0.0f ? 1.0f / top : 0.0f;
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        uint32_t f = 0;
+        if constexpr (NG > 1) {
+          const float x = sc[k * 32 / C::G] * inv;
+          f = float2_to_half2_bits(x, x);
+        }
+        const uint32_t words[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4 h = codes_to_half(words[j]);
+          if constexpr (NG > 1)
+            h = make_uint4(hmul2(h.x, f), hmul2(h.y, f), hmul2(h.z, f), hmul2(h.w, f));
+          const int c = (k & 1) * 4 + j;  // 16-byte column of the 128
+          sts128(tile + uint32_t(k / 2) * 16384 + uint32_t(t) * 128 +
+                     (uint32_t(c ^ (t & 7)) << 4),
+                 h.x, h.y, h.z, h.w);
+        }
+      }
+      fence_proxy_async_smem();
+    };
+    auto largest = [](const float (&s)[NG]) {
+      float x = s[0];
+#pragma unroll
+      for (int j = 1; j < NG; ++j) x = fmaxf(x, s[j]);
+      return x;
+    };
+    int vexp = -126;
+    wait(sh.dfull[0], 0);
+    load(0);
+    for (int i = 0; i < n; ++i) {
+      if (sh.tiles[i % kPcRing].starts) vexp = -126;
+      const float ktop = largest(ksc), vtop = largest(vsc);
+      // the V scales of the tile under a power of two that only grows
+      float x = vtop;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+      if (lane == 0) sh.wmax[i & 1][warp - C::W_DEQ] = x;
+      named_sync(3, 128);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.wmax[i & 1][w]);
+      vexp = max(vexp, min(int(__float_as_uint(x) >> 23) - 126, 126));
+      const float vmul = __uint_as_float(uint32_t(127 - vexp) << 23);
+      // ring of four: the softmax of tile i - 4 is behind V's wait of tile i - 1
+      sh.ks[i & 3][t] = ktop;
+      sh.vs[i & 3][t] = vtop * vmul;
+      if (t == 0) sh.vexp[i & 3] = vexp;
+      arrive(sh.scfull[i & 3]);
+      if (i >= KS) wait(sh.kfree[i % KS], i / KS - 1);
+      convert(kreg, ksc, ktop, sbase + C::oK + (i % KS) * C::TILE);
+      arrive(sh.kfull[i % KS]);
+      if (i >= KS) wait(sh.vfree[i % KS], i / KS - 1);
+      convert(vreg, vsc, vtop, sbase + C::oV + (i % KS) * C::TILE);
+      arrive(sh.vfull[i % KS]);
+      if (i + 1 < n) {
+        wait(sh.dfull[(i + 1) % kPcRing], (i + 1) / kPcRing);
+        load(i + 1);
+      }
+    }
+  } else {
+    // ---------------- softmax: a thread a query row ----------------
+    const int x = NT == 2 ? warp >> 2 : 0, w4 = warp & 3;
+    const uint32_t tlane = tmem + (uint32_t(w4) << 21);
+    const uint32_t tO = tlane + C::colO + x * 128;
+    const uint32_t qtile = sbase + C::oQ + x * C::TILE;
+    const uint32_t stage = qtile + w4 * 4096;  // this warp's rows of it, 4 KB of every 16
+    float m = 0.0f, l = 0.0f, rowc = 0.0f;
+    int used = 0, item = -1, vexp = 0, pos = 0;
+    bool active = false;
+    for (int i = 0; i < n; ++i) {
+      wait(sh.dfull[i % kPcRing], i / kPcRing);
+      const PcTile& e = sh.tiles[i % kPcRing];
+      const int rows = e.rows - x * 128;  // of this row tile
+      if (e.starts) {
+        // ---- this warp's queries ----
+        ++item;
+        active = rows > 0;
+        const int nr = min(max(rows - w4 * 32, 0), 32);
+        rowc = 0.0f;
+        auto queries = [&](auto rot) {
+          constexpr int ROT = decltype(rot)::value;
+          WideLane<D, ROT> L;
+          L.init(a.signs, lane);
+          for (int r = 0; r < nr; ++r) {
+            const int g = e.row0 + x * 128 + w4 * 32 + r, tok = g / a.n_q;
+            const uint16_t* src = a.q + (int64_t(e.c0) + tok) * a.q_stride +
+                                  (int64_t(e.head) * a.n_q + (g - tok * a.n_q)) * D;
+            const float f = pc_query<D, ROT>(a, src, qtile, w4 * 32 + r, L);
+            if (lane == r) rowc = f;
+          }
+        };
+        if (a.rot == kRotSRFT)
+          queries(std::integral_constant<int, kRotSRFT>{});
+        else
+          queries(std::integral_constant<int, kRotSRHT>{});
+        fence_proxy_async_smem();
+        if (active) arrive(sh.qfull[x]);
+        pos = e.p0 + (e.row0 + x * 128 + min(w4 * 32 + lane, max(rows - 1, 0))) / a.n_q;
+        m = -3e38f;
+        l = 0.0f;
+        vexp = -126;
+      }
+      if (active) {
+        const int slot = NT == 2 ? x : i & 1;
+        const uint32_t tS = tlane + slot * 128;
+        wait(sh.sdone[slot], NT == 2 ? used : i >> 1);
+        wait(sh.scfull[i & 3], i >> 2);
+        tc_fence_after();
+        const uint32_t ksa = smem_u32(sh.ks[i & 3]), vsa = smem_u32(sh.vs[i & 3]);
+        // first and last position of the warp's rows decide on masks
+        const int pf = __shfl_sync(kFull, pos, 0), pl = __shfl_sync(kFull, pos, 31);
+        const bool whole = e.t0 + KT - 1 <= pf && (a.window == 0 || e.t0 > pl - a.window) &&
+                           e.have == 0xFFu;
+        const int hi = min(pos, e.len - 1) - e.t0;                     // last column seen
+        const int lo = a.window > 0 ? pos - a.window + 1 - e.t0 : 0;   // first
+        auto seen = [&](int c) {
+          return c <= hi && c >= lo && (e.have >> (c >> 4) & 1u);
+        };
+        // ---- the row's maximum ----
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < KT; c += 32) {
+          uint32_t s[32];
+          tmem_ld<32>(tS + c, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const uint4 k = lds128(ksa + (c + j) * 4);
+            float v[4] = {__uint_as_float(s[j]) * __uint_as_float(k.x),
+                          __uint_as_float(s[j + 1]) * __uint_as_float(k.y),
+                          __uint_as_float(s[j + 2]) * __uint_as_float(k.z),
+                          __uint_as_float(s[j + 3]) * __uint_as_float(k.w)};
+            if (!whole) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                if (!seen(c + j + b)) v[b] = -INFINITY;
+            }
+            top = max3f(top, v[0], v[1]);
+            top = max3f(top, v[2], v[3]);
+          }
+        }
+        top *= rowc;  // (0 for rows that are not there)
+        if (!(top > -INFINITY)) top = -3e38f;
+        const int ve = sh.vexp[i & 3];
+        // ---- rescale the accumulators where a reference moved ----
+        const bool moved = top > m + 8.0f;
+        if (__any_sync(kFull, moved) || ve != vexp) {
+          const float mn = moved ? top : m;
+          const float f = ex2(m - mn);
+          const float fo = f * ex2(float(max(vexp - ve, -200)));
+          l *= f;
+          m = mn;
+          vexp = ve;
+          if (!e.starts) {
+            wait(sh.odone[x], NT == 2 ? used - 1 : i - 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld<32>(tO + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
+              tmem_st32(tO + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // ---- weights ----
+        const f2 rc2 = mk2(rowc, rowc), nm2 = mk2(-m, -m);
+        f2 l2 = mk2(0.0f, 0.0f);
+#pragma unroll 1
+        for (int c = 0; c < KT; c += 32) {
+          uint32_t s[32], p[16];
+          tmem_ld<32>(tS + c, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const uint4 k = lds128(ksa + (c + j) * 4), v = lds128(vsa + (c + j) * 4);
+#pragma unroll
+            for (int b = 0; b < 4; b += 2) {
+              const f2 kk = b == 0 ? mk2(__uint_as_float(k.x), __uint_as_float(k.y))
+                                   : mk2(__uint_as_float(k.z), __uint_as_float(k.w));
+              const f2 vv = b == 0 ? mk2(__uint_as_float(v.x), __uint_as_float(v.y))
+                                   : mk2(__uint_as_float(v.z), __uint_as_float(v.w));
+              const f2 t = mul2(mk2(__uint_as_float(s[j + b]), __uint_as_float(s[j + b + 1])), kk);
+              const f2 z = fma2(t, rc2, nm2);
+              float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
+              if (!whole) {
+                if (!seen(c + j + b)) p0 = 0.0f;
+                if (!seen(c + j + b + 1)) p1 = 0.0f;
+              }
+              const f2 pp = mk2(p0, p1);
+              l2 = add2(l2, pp);
+              const f2 wv = mul2(pp, vv);
+              p[(j + b) / 2] = float2_to_half2_bits(lo2(wv), hi2(wv));
+            }
+          }
+          // over columns of S that have been read
+          tmem_st16(tS + c / 2, p);
+        }
+        l += lo2(l2) + hi2(l2);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(sh.pfull[slot]);
+        ++used;
+      }
+      if (!e.ends) {
+        arrive(sh.dfree[i % kPcRing]);
+        continue;
+      }
+      // ---- end of the item, or of the block's share of it ----
+      if (active) {
+        wait(sh.odone[x], NT == 2 ? used - 1 : i);
+        tc_fence_after();
+        const bool began_here = item > 0 || sh.begun == run.begin;
+        const bool complete = e.last && began_here;
+        const float unit = ex2(float(vexp));  // of the accumulators
+        const int nr = min(max(rows - w4 * 32, 0), 32);
+        float* slot = part_slot<D, M>(a, blockIdx.x, began_here ? 1 : 0);
+        const int r0 = x * 128 + w4 * 32;  // first row in the item
+        if (!complete && lane < nr) slot[r0 + lane] = m, slot[M + r0 + lane] = l;
+        const float fin = complete ? (l > 0.0f ? unit / l : 0.0f) : unit;
+        auto results = [&](auto rot) {
+          constexpr int ROT = decltype(rot)::value;
+          WideLane<D, ROT> L;
+          L.init(a.signs, lane);
+          constexpr int W = D / 32;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {  // rows 0..15, then 16..31, through shared memory
+            __syncwarp();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld<32>(tO + c, o);
+              tmem_wait_ld();
+              if ((lane >> 4) == h) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                  const uint32_t off = uint32_t(lane & 15) * (D * 4) +
+                                       ((uint32_t((c + j) / 4) ^ uint32_t(lane & 7)) << 4);
+                  sts128(stage + (off >> 12) * 16384 + (off & 4095),
+                         __float_as_uint(__uint_as_float(o[j]) * fin),
+                         __float_as_uint(__uint_as_float(o[j + 1]) * fin),
+                         __float_as_uint(__uint_as_float(o[j + 2]) * fin),
+                         __float_as_uint(__uint_as_float(o[j + 3]) * fin));
+                }
+              }
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int r = 0; r < 16 && h * 16 + r < nr; ++r) {
+              auto value = [&](int d) {
+                const int c = pc_col(d);
+                const uint32_t off = uint32_t(r) * (D * 4) +
+                                     ((uint32_t(c / 4) ^ uint32_t(r & 7)) << 4) + (c & 3) * 4;
+                return __uint_as_float(lds32(stage + (off >> 12) * 16384 + (off & 4095)));
+              };
+              const int g = r0 + h * 16 + r;
+              if (complete) {
+                float Y[W];
+#pragma unroll
+                for (int w = 0; w < W; ++w) Y[w] = value(L.k2 * W + w) * Wide<D, ROT>::KAPPA;
+                pd_store<D, ROT>(a, Y, L, out_row(a, e.c0, e.head, e.row0 + g));
+              } else {
+                for (int d = lane; d < D; d += 32) slot[2 * M + g * D + d] = value(d);
+              }
+            }
+          }
+        };
+        if (a.rot == kRotSRFT)
+          results(std::integral_constant<int, kRotSRFT>{});
+        else
+          results(std::integral_constant<int, kRotSRHT>{});
+        if (e.last && !began_here && tid == 0) {
+          join->c0 = e.c0;
+          join->head = e.head;
+          join->row0 = e.row0;
+          join->rows = e.rows;
+          join->first_block = block_of(sh.begun, run.total, run.blocks);
+        }
+        tc_fence_before();
+      }
+      arrive(sh.dfree[i % kPcRing]);
+    }
+  }
+  if (!ok && lane == 0) atomicOr(status, kPagedTimeout);
+  pdl_release();
+  tc_fence_before();
+  __syncthreads();  // every use of tensor memory is over
+  if (warp == C::W_MMA) tmem_free(tmem, 512);
+}
+
+}  // namespace kvq
