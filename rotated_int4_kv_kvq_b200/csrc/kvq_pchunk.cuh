@@ -43,8 +43,13 @@ struct Pc {
   static constexpr int TILE = NCH * 16384;      // Q tile, K or V: 128 rows
   static constexpr int oQ = 0, oK = NT * TILE, oV = oK + KS * TILE;
   static constexpr int SMEM = oV + KS * TILE + 1024;
-  static constexpr int WARPS = NT * 4 + 6;
+  static constexpr int WARPS = NT * 4 + 8;      // whole warpgroups, two warps idle
   static constexpr int THREADS = WARPS * 32;
+  // Registers a thread: the softmax holds a row's 64 words of P and two pieces
+  // of S.  256 x 176 + 256 x 80 is what 512 threads are launched with (at d =
+  // 256 the 384 threads have 168 each).
+  static constexpr bool SPLIT = NT == 2;
+  static constexpr int REGS_MORE = 176, REGS_LESS = 80;
   static constexpr int W_DEQ = NT * 4, W_MMA = W_DEQ + 4, W_PAGE = W_MMA + 1;
   static constexpr uint32_t colO = 256;         // tensor memory: S/P slots, then O
   static_assert(SMEM + 4096 <= 232448, "shared memory");
@@ -62,6 +67,8 @@ struct PcShared {
   uint64_t dfull[kPcRing], dfree[kPcRing];
   uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
   uint64_t scfull[4];            // scales
+  // By slot (a row tile, or tiles in turn: the scores of a tile are issued before
+  // the values of the one before, so one barrier could be two phases behind).
   uint64_t qfull[2], sdone[2], pfull[2], odone[2];
   PcTile tiles[kPcRing];
   uint32_t tmem;
@@ -122,6 +129,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Registers of this warpgroup's threads from here on.
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Rotates one query row into the Q tile; returns (in every lane) the factor
@@ -214,7 +231,10 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
     if (lane == 0) mbar_arrive(smem_u32(&b));
   };
 
-  if (warp == C::W_PAGE) {
+  if (warp > C::W_PAGE) {
+    if constexpr (C::SPLIT) regs_dec<C::REGS_LESS>();  // idle
+  } else if (warp == C::W_PAGE) {
+    if constexpr (C::SPLIT) regs_dec<C::REGS_LESS>();
     // ---------------- pages: what each tile is, and where ----------------
     Cursor<M, KT> c;
     c.seek(a, run.seq, run.off);
@@ -255,6 +275,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
       if (i + 1 < n && ++c.tile == c.count) c.next_item(a);
     }
   } else if (warp == C::W_MMA) {
+    if constexpr (C::SPLIT) regs_dec<C::REGS_LESS>();
     // ---------------- MMA issue ----------------
     constexpr uint32_t idS = instr_desc(kAccF32, kFmtF16, kFmtF16, false, false, 128, KT);
     constexpr uint32_t idO = instr_desc(kAccF32, kFmtF16, kFmtF16, false, true, 128, D);
@@ -283,7 +304,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         for (int s = 0; s < KT / 16; ++s)
           mma_f16_ts(tmem + C::colO + x * 128, tmem + slot * 128 + s * 8,
                      smem_desc(v + s * 2048, 16384, 1024, kSw128), idO, !first || s > 0);
-        mma_commit(bar(sh.odone[x]));
+        mma_commit(bar(sh.odone[slot]));
         if (x == NT - 1 || !two) mma_commit(bar(sh.vfree[i % KS]));
       }
       __syncwarp();
@@ -323,6 +344,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
       }
     }
   } else if (warp >= C::W_DEQ) {
+    if constexpr (C::SPLIT) regs_dec<C::REGS_LESS>();
     // ---------------- packed codes -> fp16 operands, a thread a token ----------------
     const int t = tid - C::W_DEQ * 32;
     constexpr int NP = D / 32;  // 16-byte pieces of a row
@@ -404,6 +426,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
       }
     }
   } else {
+    if constexpr (C::SPLIT) regs_inc<C::REGS_MORE>();
     // ---------------- softmax: a thread a query row ----------------
     const int x = NT == 2 ? warp >> 2 : 0, w4 = warp & 3;
     const uint32_t tlane = tmem + (uint32_t(w4) << 21);
@@ -442,7 +465,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         fence_proxy_async_smem();
         if (active) arrive(sh.qfull[x]);
         pos = e.p0 + (e.row0 + x * 128 + min(w4 * 32 + lane, max(rows - 1, 0))) / a.n_q;
-        m = -3e38f;
+        m = lane < nr ? -3e38f : 0.0f;  // (what rows that are not there hold moves nothing)
         l = 0.0f;
         vexp = -126;
       }
@@ -462,43 +485,85 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         auto seen = [&](int c) {
           return c <= hi && c >= lo && (e.have >> (c >> 4) & 1u);
         };
-        // ---- the row's maximum ----
-        float top = -INFINITY;
+        const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[i & 3]);
+        const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[i & 3]);
+        // ---- the row's maximum (only where a reference has to move) ----
+        auto largest = [&]() {
+          float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < KT; c += 32) {
-          uint32_t s[32];
-          tmem_ld<32>(tS + c, s);
-          tmem_wait_ld();
+          for (int c = 0; c < KT; c += 32) {
+            uint32_t s[32];
+            tmem_ld<32>(tS + c, s);
+            tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const uint4 k = lds128(ksa + (c + j) * 4);
-            float v[4] = {__uint_as_float(s[j]) * __uint_as_float(k.x),
-                          __uint_as_float(s[j + 1]) * __uint_as_float(k.y),
-                          __uint_as_float(s[j + 2]) * __uint_as_float(k.z),
-                          __uint_as_float(s[j + 3]) * __uint_as_float(k.w)};
-            if (!whole) {
+            for (int j = 0; j < 32; j += 4) {
+              const float4 k = ks4[(c + j) / 4];
+              const float kk[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
               for (int b = 0; b < 4; ++b)
-                if (!seen(c + j + b)) v[b] = -INFINITY;
+                if (whole || seen(c + j + b)) top = fmaxf(top, __uint_as_float(s[j + b]) * kk[b]);
             }
-            top = max3f(top, v[0], v[1]);
-            top = max3f(top, v[2], v[3]);
           }
-        }
-        top *= rowc;  // (0 for rows that are not there)
-        if (!(top > -INFINITY)) top = -3e38f;
+          top *= rowc;  // (0 for rows that are not there)
+          return top > -INFINITY ? top : -3e38f;
+        };
+        // ---- weights against the reference; returns the largest exponent ----
+        uint32_t p[KT / 2];
+        f2 l2;
+        auto weights = [&](auto masks) {
+          constexpr bool MASK = decltype(masks)::value;
+          const f2 rc2 = mk2(rowc, rowc), nm2 = mk2(-m, -m);
+          l2 = mk2(0.0f, 0.0f);
+          float zmax = -INFINITY;
+          uint32_t s[2][32];
+          tmem_ld<32>(tS, s[0]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < KT; c += 32) {
+            uint32_t(&cur)[32] = s[(c / 32) & 1];
+            if (c + 32 < KT) tmem_ld<32>(tS + c + 32, s[(c / 32 + 1) & 1]);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 k = ks4[(c + j) / 4], v = vs4[(c + j) / 4];
+#pragma unroll
+              for (int b = 0; b < 4; b += 2) {
+                const f2 kk = b == 0 ? mk2(k.x, k.y) : mk2(k.z, k.w);
+                const f2 vv = b == 0 ? mk2(v.x, v.y) : mk2(v.z, v.w);
+                const f2 t =
+                    mul2(mk2(__uint_as_float(cur[j + b]), __uint_as_float(cur[j + b + 1])), kk);
+                const f2 z = fma2(t, rc2, nm2);
+                float z0 = lo2(z), z1 = hi2(z);
+                if constexpr (MASK) {
+                  if (!seen(c + j + b)) z0 = -INFINITY;
+                  if (!seen(c + j + b + 1)) z1 = -INFINITY;
+                }
+                zmax = max3f(zmax, z0, z1);
+                const f2 pp = mk2(ex2(z0), ex2(z1));
+                l2 = add2(l2, pp);
+                const f2 wv = mul2(pp, vv);
+                p[(c + j + b) / 2] = float2_to_half2_bits(lo2(wv), hi2(wv));
+              }
+            }
+            if (c + 32 < KT) tmem_wait_ld();
+          }
+          return zmax;
+        };
         const int ve = sh.vexp[i & 3];
-        // ---- rescale the accumulators where a reference moved ----
-        const bool moved = top > m + 8.0f;
-        if (__any_sync(kFull, moved) || ve != vexp) {
-          const float mn = moved ? top : m;
+        for (bool moved = false;; moved = true) {  // twice at most
+          if (ve == vexp) {
+            const float zmax = whole ? weights(std::false_type{}) : weights(std::true_type{});
+            if (moved || !__any_sync(kFull, zmax > 8.0f)) break;
+          }
+          // ---- a reference moves: rescale the accumulators ----
+          const float top = largest();
+          const float mn = top > m + 8.0f ? top : m;
           const float f = ex2(m - mn);
           const float fo = f * ex2(float(max(vexp - ve, -200)));
           l *= f;
           m = mn;
           vexp = ve;
           if (!e.starts) {
-            wait(sh.odone[x], NT == 2 ? used - 1 : i - 1);
+            wait(sh.odone[NT == 2 ? x : (i - 1) & 1], NT == 2 ? used - 1 : (i - 1) >> 1);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -512,40 +577,17 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
             tmem_wait_st();
           }
         }
-        // ---- weights ----
-        const f2 rc2 = mk2(rowc, rowc), nm2 = mk2(-m, -m);
-        f2 l2 = mk2(0.0f, 0.0f);
-#pragma unroll 1
-        for (int c = 0; c < KT; c += 32) {
-          uint32_t s[32], p[16];
-          tmem_ld<32>(tS + c, s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const uint4 k = lds128(ksa + (c + j) * 4), v = lds128(vsa + (c + j) * 4);
-#pragma unroll
-            for (int b = 0; b < 4; b += 2) {
-              const f2 kk = b == 0 ? mk2(__uint_as_float(k.x), __uint_as_float(k.y))
-                                   : mk2(__uint_as_float(k.z), __uint_as_float(k.w));
-              const f2 vv = b == 0 ? mk2(__uint_as_float(v.x), __uint_as_float(v.y))
-                                   : mk2(__uint_as_float(v.z), __uint_as_float(v.w));
-              const f2 t = mul2(mk2(__uint_as_float(s[j + b]), __uint_as_float(s[j + b + 1])), kk);
-              const f2 z = fma2(t, rc2, nm2);
-              float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
-              if (!whole) {
-                if (!seen(c + j + b)) p0 = 0.0f;
-                if (!seen(c + j + b + 1)) p1 = 0.0f;
-              }
-              const f2 pp = mk2(p0, p1);
-              l2 = add2(l2, pp);
-              const f2 wv = mul2(pp, vv);
-              p[(j + b) / 2] = float2_to_half2_bits(lo2(wv), hi2(wv));
-            }
-          }
-          // over columns of S that have been read
-          tmem_st16(tS + c / 2, p);
-        }
         l += lo2(l2) + hi2(l2);
+        // P over S, which has been read
+        {
+          uint32_t h[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) h[j] = p[j];
+          tmem_st32(tS, h);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) h[j] = p[32 + j];
+          tmem_st32(tS + 32, h);
+        }
         tmem_wait_st();
         tc_fence_before();
         arrive(sh.pfull[slot]);
@@ -557,7 +599,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
       }
       // ---- end of the item, or of the block's share of it ----
       if (active) {
-        wait(sh.odone[x], NT == 2 ? used - 1 : i);
+        wait(sh.odone[NT == 2 ? x : i & 1], NT == 2 ? used - 1 : i >> 1);
         tc_fence_after();
         const bool began_here = item > 0 || sh.begun == run.begin;
         const bool complete = e.last && began_here;
