@@ -27,6 +27,7 @@
 // up.  P overwrites S in tensor memory and is read from there.
 #pragma once
 
+#include "kvq_codec.cuh"
 #include "kvq_pdecode.cuh"
 
 namespace kvq {
@@ -45,9 +46,9 @@ struct Pc {
   static constexpr int SMEM = oV + KS * TILE + 1024;
   static constexpr int WARPS = NT * 4 + 8;      // whole warpgroups, two warps idle
   static constexpr int THREADS = WARPS * 32;
-  // Registers a thread: the softmax holds a row's 64 words of P and two pieces
-  // of S.  256 x 176 + 256 x 80 is what 512 threads are launched with (at d =
-  // 256 the 384 threads have 168 each).
+  // Registers a thread: the softmax threads hold a whole row when they rotate it.
+  // 256 x 176 + 256 x 80 is what 512 threads are launched with (at d = 256 the
+  // 384 threads have 168 each).
   static constexpr bool SPLIT = NT == 2;
   static constexpr int REGS_MORE = 176, REGS_LESS = 80;
   static constexpr int W_DEQ = NT * 4, W_MMA = W_DEQ + 4, W_PAGE = W_MMA + 1;
@@ -76,6 +77,7 @@ struct PcShared {
   float ks[4][128], vs[4][128];  // by tile: K scales; V scales over 2^vexp
   int vexp[4];
   float wmax[2][4];
+  uint32_t sign_in[64], sign_out[64];  // d <= 128: sign masks of a row's words
   int64_t scratch[16 + 4];
 };
 
@@ -141,7 +143,17 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Rotates one query row into the Q tile; returns (in every lane) the factor
+// Factor for a row whose largest rotated value is `top`: a power of two that
+// brings it into [2^8, 2^9), far from fp16's smallest and largest, with the sign
+// of the softmax scale; `back` undoes it and applies the scale.
+__device__ __forceinline__ float pc_scale(float top, float qscale, float& back) {
+  const int e = min(max(int(__float_as_uint(top) >> 23), 20), 234);
+  back = __uint_as_float(uint32_t(e - 8) << 23) * fabsf(qscale);  // 2^(e - 135)
+  const float mul = __uint_as_float(uint32_t(262 - e) << 23);
+  return qscale < 0.0f ? -mul : mul;
+}
+
+// Rotates one query row into the Q tile, a warp a row; returns (in every lane) the factor
 // from its products to log2 scores.
 template <int D, int ROT>
 __device__ __forceinline__ float pc_query(const PagedAttnArgs& a, const uint16_t* src, uint32_t tile,
@@ -162,11 +174,8 @@ __device__ __forceinline__ float pc_query(const PagedAttnArgs& a, const uint16_t
   for (int w = 0; w < P::W; ++w) top = fmaxf(top, fabsf(Y[w]));
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  // largest value into [2^8, 2^9): far from fp16's smallest and largest
-  const int e = min(max(int(__float_as_uint(top) >> 23), 20), 234);
-  const float mul = __uint_as_float(uint32_t(262 - e) << 23);   // 2^(135 - e)
-  const float back = __uint_as_float(uint32_t(e - 8) << 23);    // its inverse
-  const float sg = a.qscale < 0.0f ? -mul : mul;
+  float back;
+  const float sg = pc_scale(top, a.qscale, back);
 #pragma unroll
   for (int w = 0; w < P::W; ++w) {
     const int c = pc_col(L.k2 * P::W + w);
@@ -176,7 +185,93 @@ __device__ __forceinline__ float pc_query(const PagedAttnArgs& a, const uint16_t
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const uint16_t*>(&h))
                  : "memory");
   }
-  return back * P::KAPPA * fabsf(a.qscale);
+  return back * P::KAPPA;
+}
+
+// d <= 128: a thread rotates its own row, in registers (the two-lane real FFT
+// codelets, or a Walsh-Hadamard network), into the Q tile.  Returns the factor
+// from the row's products to log2 scores.
+template <int D, int ROT>
+__device__ __forceinline__ float pc_query_row(const PagedAttnArgs& a, const uint16_t* src,
+                                              uint32_t tile, int r, const uint32_t* sign) {
+  using C = Cfg<D, ROT, 1>;
+  f2 u[C::NW], Y[C::P];
+#pragma unroll
+  for (int c = 0; c < C::NW / 4; ++c) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = w[j] ^ sign[4 * c + j];
+      const float2 f = a.dtype == kDtF16 ? pair_to_float2<kDtF16>(x) : pair_to_float2<kDtBF16>(x);
+      u[4 * c + j] = mk2(f.x, f.y);
+    }
+  }
+  rotate_fwd<C>(u, 0, Y);
+  const float top = absmax2<C::P>(Y);
+  float back;
+  const float sg = pc_scale(top, a.qscale, back);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {  // columns 0 4 1 5 2 6 3 7 of each eight
+    const f2 p = Y[4 * i], q = Y[4 * i + 1], s = Y[4 * i + 2], t = Y[4 * i + 3];
+    sts128(tile + uint32_t(i >> 3) * 16384 + uint32_t(r) * 128 + (uint32_t((i ^ r) & 7) << 4),
+           float2_to_half2_bits(lo2(p) * sg, lo2(s) * sg),
+           float2_to_half2_bits(hi2(p) * sg, hi2(s) * sg),
+           float2_to_half2_bits(lo2(q) * sg, lo2(t) * sg),
+           float2_to_half2_bits(hi2(q) * sg, hi2(t) * sg));
+  }
+  return back * C::KAPPA_INV;  // both ways the same
+}
+
+// The way back: a row's accumulators (columns 0 4 1 5 2 6 3 7 of each eight) as
+// coordinate pairs times `mul`.
+template <int D>
+__device__ __forceinline__ void pc_row(uint32_t acc, float mul, f2 (&Y)[D / 2]) {
+#pragma unroll
+  for (int c = 0; c < D; c += 32) {
+    uint32_t o[32];
+    tmem_ld<32>(acc + c, o);
+    tmem_wait_ld();
+    const f2 m2 = mk2(mul, mul);
+    auto pair = [&](int x, int y) {
+      return mul2(mk2(__uint_as_float(o[x]), __uint_as_float(o[y])), m2);
+    };
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      f2* y = Y + c / 2 + 4 * g;
+      y[0] = pair(8 * g, 8 * g + 2);
+      y[1] = pair(8 * g + 4, 8 * g + 6);
+      y[2] = pair(8 * g + 1, 8 * g + 3);
+      y[3] = pair(8 * g + 5, 8 * g + 7);
+    }
+  }
+}
+template <int D, int ROT>
+__device__ __forceinline__ void pc_result_row(const PagedAttnArgs& a, f2 (&Y)[D / 2], uint16_t* dst,
+                                              const uint32_t* sign) {
+  using C = Cfg<D, ROT, 1>;
+  f2 x[C::NW];
+  if constexpr (ROT == kRotSRHT) {
+    fwht<C::P>(Y);
+#pragma unroll
+    for (int j = 0; j < C::NW; ++j) x[j] = Y[j];
+  } else {
+    f2 z[C::NW];
+    split_lanes_inv<D>(Y, z);
+    RFFT2<D / 2>::inv(z, x);
+  }
+#pragma unroll
+  for (int c = 0; c < C::NW / 4; ++c) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f2 v = x[4 * c + j];
+      w[j] = (a.dtype == kDtF16 ? float2_to_pair<kDtF16>(lo2(v), hi2(v))
+                                : float2_to_pair<kDtBF16>(lo2(v), hi2(v))) ^
+             sign[4 * c + j];
+    }
+    reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 template <int D, int NG>
@@ -210,6 +305,14 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
     fence_mbar_init();
   }
   pdl_wait();  // no global access before the previous kernel completes
+  if constexpr (D <= 128) {
+    if (tid < D / 2) {
+      sh.sign_in[tid] = a.rot == kRotSRFT ? load_mask_word<Cfg<D, kRotSRFT, 1>>(a.signs, 0, tid)
+                                          : load_mask_word<Cfg<D, kRotSRHT, 1>>(a.signs, 0, tid);
+      sh.sign_out[tid] = a.rot == kRotSRFT ? store_mask_word<Cfg<D, kRotSRFT, 1>>(a.signs, 0, tid)
+                                           : store_mask_word<Cfg<D, kRotSRHT, 1>>(a.signs, 0, tid);
+    }
+  }
   const Run run = find_run<M, KT, C::THREADS>(a, blockIdx.x, gridDim.x, sh.scratch, status);
   JoinInfo* join = a.join + blockIdx.x;
   if (tid == 0) join->first_block = -1;
@@ -286,7 +389,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
       if (lane == 0) {
         tc_fence_after();
         const uint32_t q = sbase + C::oQ + x * C::TILE, k = sbase + C::oK + (i % KS) * C::TILE;
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < D / 16; ++s)
           mma_f16(tmem + slot * 128, smem_desc(q + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128),
                   smem_desc(k + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128), idS, s > 0);
@@ -300,7 +403,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
       if (lane == 0) {
         tc_fence_after();
         const uint32_t v = sbase + C::oV + (i % KS) * C::TILE;
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < KT / 16; ++s)
           mma_f16_ts(tmem + C::colO + x * 128, tmem + slot * 128 + s * 8,
                      smem_desc(v + s * 2048, 16384, 1024, kSw128), idO, !first || s > 0);
@@ -448,14 +551,21 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         rowc = 0.0f;
         auto queries = [&](auto rot) {
           constexpr int ROT = decltype(rot)::value;
-          WideLane<D, ROT> L;
-          L.init(a.signs, lane);
-          for (int r = 0; r < nr; ++r) {
+          auto source = [&](int r) {
             const int g = e.row0 + x * 128 + w4 * 32 + r, tok = g / a.n_q;
-            const uint16_t* src = a.q + (int64_t(e.c0) + tok) * a.q_stride +
-                                  (int64_t(e.head) * a.n_q + (g - tok * a.n_q)) * D;
-            const float f = pc_query<D, ROT>(a, src, qtile, w4 * 32 + r, L);
-            if (lane == r) rowc = f;
+            return a.q + (int64_t(e.c0) + tok) * a.q_stride +
+                   (int64_t(e.head) * a.n_q + (g - tok * a.n_q)) * D;
+          };
+          if constexpr (D <= 128) {
+            if (lane < nr)
+              rowc = pc_query_row<D, ROT>(a, source(lane), qtile, w4 * 32 + lane, sh.sign_in);
+          } else {
+            WideLane<D, ROT> L;
+            L.init(a.signs, lane);
+            for (int r = 0; r < nr; ++r) {
+              const float f = pc_query<D, ROT>(a, source(r), qtile, w4 * 32 + r, L);
+              if (lane == r) rowc = f;
+            }
           }
         };
         if (a.rot == kRotSRFT)
@@ -487,41 +597,74 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         };
         const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[i & 3]);
         const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[i & 3]);
-        // ---- the row's maximum (only where a reference has to move) ----
-        auto largest = [&]() {
-          float top = -INFINITY;
+        // ---- the row's maximum, and where a reference moves, the accumulators ----
+        const int ve = sh.vexp[i & 3];
+        {
+          // (All loops over columns are rolled: what the roles run per tile has to
+          // stay in the instruction cache.  Unrolled, one pass took 1.6 times as
+          // long.)
+          float top = -INFINITY, top1 = -INFINITY;
+          auto largest = [&](auto masks) {
+            constexpr bool MASK = decltype(masks)::value;
 #pragma unroll 1
-          for (int c = 0; c < KT; c += 32) {
-            uint32_t s[32];
-            tmem_ld<32>(tS + c, s);
-            tmem_wait_ld();
+            for (int c = 0; c < KT; c += 32) {
+              uint32_t s[32];
+              tmem_ld<32>(tS + c, s);
+              tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 k = ks4[(c + j) / 4];
-              const float kk[4] = {k.x, k.y, k.z, k.w};
+              for (int j = 0; j < 32; j += 4) {
+                const float4 k = ks4[(c + j) / 4];
+                f2 u = mul2(mk2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), mk2(k.x, k.y));
+                f2 w = mul2(mk2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), mk2(k.z, k.w));
+                if constexpr (MASK) {
+                  u = mk2(seen(c + j) ? lo2(u) : -INFINITY, seen(c + j + 1) ? hi2(u) : -INFINITY);
+                  w = mk2(seen(c + j + 2) ? lo2(w) : -INFINITY, seen(c + j + 3) ? hi2(w) : -INFINITY);
+                }
+                top = max3f(top, lo2(u), hi2(u));
+                top1 = max3f(top1, lo2(w), hi2(w));
+              }
+            }
+          };
+          if (whole)
+            largest(std::false_type{});
+          else
+            largest(std::true_type{});
+          top = fmaxf(top, top1) * rowc;  // (0 for rows that are not there)
+          if (!(top > -INFINITY)) top = -3e38f;
+          const bool moved = top > m + 8.0f;
+          if (__any_sync(kFull, moved) || ve != vexp) {
+            const float mn = moved ? top : m;
+            const float f = ex2(m - mn);
+            const float fo = f * ex2(float(max(vexp - ve, -200)));
+            l *= f;
+            m = mn;
+            vexp = ve;
+            if (!e.starts) {
+              wait(sh.odone[NT == 2 ? x : (i - 1) & 1], NT == 2 ? used - 1 : (i - 1) >> 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld<32>(tO + c, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (whole || seen(c + j + b)) top = fmaxf(top, __uint_as_float(s[j + b]) * kk[b]);
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
+                tmem_st32(tO + c, o);
+              }
+              tmem_wait_st();
             }
           }
-          top *= rowc;  // (0 for rows that are not there)
-          return top > -INFINITY ? top : -3e38f;
-        };
-        // ---- weights against the reference; returns the largest exponent ----
-        uint32_t p[KT / 2];
-        f2 l2;
+        }
+        // ---- weights ----
         auto weights = [&](auto masks) {
           constexpr bool MASK = decltype(masks)::value;
           const f2 rc2 = mk2(rowc, rowc), nm2 = mk2(-m, -m);
-          l2 = mk2(0.0f, 0.0f);
-          float zmax = -INFINITY;
-          uint32_t s[2][32];
-          tmem_ld<32>(tS, s[0]);
-          tmem_wait_ld();
-#pragma unroll
+          f2 l2 = mk2(0.0f, 0.0f);
+#pragma unroll 1
           for (int c = 0; c < KT; c += 32) {
-            uint32_t(&cur)[32] = s[(c / 32) & 1];
-            if (c + 32 < KT) tmem_ld<32>(tS + c + 32, s[(c / 32 + 1) & 1]);
+            uint32_t s[32], p[16];
+            tmem_ld<32>(tS + c, s);
+            tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               const float4 k = ks4[(c + j) / 4], v = vs4[(c + j) / 4];
@@ -529,65 +672,27 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
               for (int b = 0; b < 4; b += 2) {
                 const f2 kk = b == 0 ? mk2(k.x, k.y) : mk2(k.z, k.w);
                 const f2 vv = b == 0 ? mk2(v.x, v.y) : mk2(v.z, v.w);
-                const f2 t =
-                    mul2(mk2(__uint_as_float(cur[j + b]), __uint_as_float(cur[j + b + 1])), kk);
+                const f2 t = mul2(mk2(__uint_as_float(s[j + b]), __uint_as_float(s[j + b + 1])), kk);
                 const f2 z = fma2(t, rc2, nm2);
                 float z0 = lo2(z), z1 = hi2(z);
                 if constexpr (MASK) {
                   if (!seen(c + j + b)) z0 = -INFINITY;
                   if (!seen(c + j + b + 1)) z1 = -INFINITY;
                 }
-                zmax = max3f(zmax, z0, z1);
                 const f2 pp = mk2(ex2(z0), ex2(z1));
                 l2 = add2(l2, pp);
                 const f2 wv = mul2(pp, vv);
-                p[(c + j + b) / 2] = float2_to_half2_bits(lo2(wv), hi2(wv));
+                p[(j + b) / 2] = float2_to_half2_bits(lo2(wv), hi2(wv));
               }
             }
-            if (c + 32 < KT) tmem_wait_ld();
+            tmem_st16(tS + c / 2, p);  // over columns of S that have been read
           }
-          return zmax;
+          l += lo2(l2) + hi2(l2);
         };
-        const int ve = sh.vexp[i & 3];
-        for (bool moved = false;; moved = true) {  // twice at most
-          if (ve == vexp) {
-            const float zmax = whole ? weights(std::false_type{}) : weights(std::true_type{});
-            if (moved || !__any_sync(kFull, zmax > 8.0f)) break;
-          }
-          // ---- a reference moves: rescale the accumulators ----
-          const float top = largest();
-          const float mn = top > m + 8.0f ? top : m;
-          const float f = ex2(m - mn);
-          const float fo = f * ex2(float(max(vexp - ve, -200)));
-          l *= f;
-          m = mn;
-          vexp = ve;
-          if (!e.starts) {
-            wait(sh.odone[NT == 2 ? x : (i - 1) & 1], NT == 2 ? used - 1 : (i - 1) >> 1);
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld<32>(tO + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
-              tmem_st32(tO + c, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        l += lo2(l2) + hi2(l2);
-        // P over S, which has been read
-        {
-          uint32_t h[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) h[j] = p[j];
-          tmem_st32(tS, h);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) h[j] = p[32 + j];
-          tmem_st32(tS + 32, h);
-        }
+        if (whole)
+          weights(std::false_type{});
+        else
+          weights(std::true_type{});
         tmem_wait_st();
         tc_fence_before();
         arrive(sh.pfull[slot]);
@@ -609,7 +714,31 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         const int r0 = x * 128 + w4 * 32;  // first row in the item
         if (!complete && lane < nr) slot[r0 + lane] = m, slot[M + r0 + lane] = l;
         const float fin = complete ? (l > 0.0f ? unit / l : 0.0f) : unit;
+        if constexpr (D <= 128) {
+          f2 Y[D / 2];
+          // (the kappa of either rotation's inverse, 1 for a partial result)
+          const float kappa = !complete            ? 1.0f
+                              : a.rot == kRotSRFT ? Cfg<D, kRotSRFT, 1>::KAPPA_INV
+                                                  : Cfg<D, kRotSRHT, 1>::KAPPA_INV;
+          pc_row<D>(tO, fin * kappa, Y);
+          if (lane < nr) {
+            if (!complete) {
+              float4* dst = reinterpret_cast<float4*>(slot + 2 * M + (r0 + lane) * D);
+#pragma unroll
+              for (int j = 0; j < D / 4; ++j)
+                dst[j] = make_float4(lo2(Y[2 * j]), hi2(Y[2 * j]), lo2(Y[2 * j + 1]),
+                                     hi2(Y[2 * j + 1]));
+            } else {
+              uint16_t* dst = out_row(a, e.c0, e.head, e.row0 + r0 + lane);
+              if (a.rot == kRotSRFT)
+                pc_result_row<D, kRotSRFT>(a, Y, dst, sh.sign_out);
+              else
+                pc_result_row<D, kRotSRHT>(a, Y, dst, sh.sign_out);
+            }
+          }
+        }
         auto results = [&](auto rot) {
+          if constexpr (D <= 128) return;
           constexpr int ROT = decltype(rot)::value;
           WideLane<D, ROT> L;
           L.init(a.signs, lane);
