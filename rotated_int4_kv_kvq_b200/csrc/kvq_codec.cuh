@@ -557,13 +557,14 @@ __device__ __forceinline__ void pair_join_inv(const f2 (&Y)[C::P], int t, f2 (&Z
 // corrected by the store-side sign mask.
 // With LAM, the values are multiplied by the store-side factor pairs at
 // `lam` (shared memory: sign / lambda, see fill_lambda) before the fp16
-// rounding, and the store path applies no sign mask.
+// rounding, and the store path applies no sign mask.  With `bf16` the words
+// are bf16 pairs instead.
 template <class C, bool LAM = false>
 __device__ __forceinline__ void rotate_inv(f2 (&Y)[C::P], int t, uint32_t (&xw)[C::NW],
-                                           uint32_t lam = 0) {
+                                           uint32_t lam = 0, bool bf16 = false) {
   auto scaled = [&](f2 v, int j) {
     if constexpr (LAM) v = mul2(v, lds_f2(lam + 8u * j));
-    return float2_to_half2_bits(lo2(v), hi2(v));
+    return bf16 ? float2_to_bf162_bits(lo2(v), hi2(v)) : float2_to_half2_bits(lo2(v), hi2(v));
   };
   // With LAM, a warp barrier after every 8 converted words: shared-memory
   // loads are not moved across it, so at most 8 lambda pairs are live at a

@@ -11,6 +11,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -305,6 +306,11 @@ __device__ __forceinline__ float2 half2_bits_to_float2(uint32_t w) {
 __device__ __forceinline__ uint32_t float2_to_half2_bits(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);  // round to nearest even, both lanes
   return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t float2_to_bf162_bits(float lo, float hi) {
+  __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&b);
 }
 
 // A pair of floats in one 64-bit register pair, operated on by the sm_100

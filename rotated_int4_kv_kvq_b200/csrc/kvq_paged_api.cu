@@ -153,12 +153,13 @@ kvq_status kvq_paged_append(const void* k, const void* v, kvq_dtype dtype, int64
   a.n_tokens = n_tokens;
   a.n_slots = cache->n_pages * cache->page_size;
   a.n_heads = cache->n_kv_heads;
+  a.dtype = dtype;
   a.page_shift = log2_page(cache->page_size);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int rot = cache->rot, g = cache->group;
-  return from_cuda(cache->d == 64    ? kvq::launch_append<64>(dtype, rot, g, a, dev.sm_count, st)
-                   : cache->d == 128 ? kvq::launch_append<128>(dtype, rot, g, a, dev.sm_count, st)
-                                     : kvq::launch_append<256>(dtype, rot, g, a, dev.sm_count, st));
+  return from_cuda(cache->d == 64    ? kvq::launch_append<64>(rot, g, a, dev.sm_count, st)
+                   : cache->d == 128 ? kvq::launch_append<128>(rot, g, a, dev.sm_count, st)
+                                     : kvq::launch_append<256>(rot, g, a, dev.sm_count, st));
 }
 
 int64_t kvq_paged_attend_workspace(int64_t n_tokens, int32_t n_kv_heads, int32_t n_q, int32_t d,

@@ -3,7 +3,7 @@
 
 namespace kvq {
 template cudaError_t launch_norm_rope<128>(int, const NormRopeArgs&, int, cudaStream_t);
-template cudaError_t launch_append<128>(int, int, int, const AppendArgs&, int, cudaStream_t);
+template cudaError_t launch_append<128>(int, int, const AppendArgs&, int, cudaStream_t);
 template cudaError_t launch_paged_attn<128>(const PagedAttnArgs&, int, int, cudaStream_t);
 template cudaError_t read_paged_status<128>(uint32_t*, bool);
 }  // namespace kvq

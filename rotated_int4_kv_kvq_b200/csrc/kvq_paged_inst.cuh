@@ -57,26 +57,7 @@ cudaError_t launch_paged(void (*kern)(KArgs...), int64_t grid, int threads, int 
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int D, int ROT, int DT>
-cudaError_t append_group(const AppendArgs& a, int group, int sm_count, cudaStream_t stream,
-                         unsigned* st) {
-  const int64_t rows = a.n_tokens * 2 * a.n_heads;
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, int64_t(sm_count) * 12));
-  switch (group) {
-    case 32: return launch_paged(kvq_append_wide_kernel<D, 32, ROT, DT>, grid, kWideThreads, 0, stream, a, st);
-    case 64: return launch_paged(kvq_append_wide_kernel<D, 64, ROT, DT>, grid, kWideThreads, 0, stream, a, st);
-    case 128:
-      if constexpr (D >= 128)
-        return launch_paged(kvq_append_wide_kernel<D, 128, ROT, DT>, grid, kWideThreads, 0, stream, a, st);
-      break;
-    case 256:
-      if constexpr (D >= 256)
-        return launch_paged(kvq_append_wide_kernel<D, 256, ROT, DT>, grid, kWideThreads, 0, stream, a, st);
-  }
-  return cudaErrorInvalidValue;
-}
-
-// Opts an attention kernel into its shared memory (once per kernel and device).
+// Opts a kernel into its shared memory (once per kernel and device).
 template <auto Kern>
 cudaError_t paged_setup(int smem) {
   constexpr int kMax = 64;
@@ -93,6 +74,50 @@ cudaError_t paged_setup(int smem) {
     done[dev] = true;
   }
   return cudaSuccess;
+}
+
+// Appending: rows of a call from which a thread (pair) a row beats a warp a row.
+// Norm, rotation and dequantized rows, one warp against one thread a row, us:
+// d = 64 at 8192 rows 6.2 against 8.5, at 16384 10.4 against 8.8, at 262144 163
+// against 60; d = 128 at 16384 13.8 against 16.8, at 32768 24.0 against 18.2, at
+// 262144 202 against 124; d = 256 at 8192 12.9 against 19.5, at 16384 22.3
+// against 20.9, at 65536 98 against 81.
+constexpr int64_t append_tile_rows(int d) { return d == 64 ? 12288 : (d == 128 ? 20480 : 14336); }
+
+template <int D, int G, int ROT>
+cudaError_t append_one(const AppendArgs& a, int sm_count, cudaStream_t stream, unsigned* st) {
+  const int64_t rows = a.n_tokens * 2 * a.n_heads;
+  if (rows >= append_tile_rows(D)) {
+    constexpr auto kern = kvq_append_tile_kernel<D, G, ROT>;
+    constexpr int smem = kAppendWarps * append_tile_bytes<D>();
+    cudaError_t e = paged_setup<kern>(smem);
+    if (e != cudaSuccess) return e;
+    constexpr int vpw = vpw_of(D);
+    const int64_t tiles = (a.n_tokens + vpw - 1) / vpw * 2 * a.n_heads;
+    const int64_t grid =
+        std::min<int64_t>((tiles + kAppendWarps - 1) / kAppendWarps, int64_t(sm_count) * 3);
+    return launch_paged(kern, grid, kAppendThreads, smem, stream, a, st);
+  }
+  const int64_t grid =
+      std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, int64_t(sm_count) * 12));
+  return a.dtype == kDtF16
+             ? launch_paged(kvq_append_wide_kernel<D, G, ROT, kDtF16>, grid, kWideThreads, 0, stream, a, st)
+             : launch_paged(kvq_append_wide_kernel<D, G, ROT, kDtBF16>, grid, kWideThreads, 0, stream, a, st);
+}
+
+template <int D, int ROT>
+cudaError_t append_group(const AppendArgs& a, int group, int sm_count, cudaStream_t stream,
+                         unsigned* st) {
+  switch (group) {
+    case 32: return append_one<D, 32, ROT>(a, sm_count, stream, st);
+    case 64: return append_one<D, 64, ROT>(a, sm_count, stream, st);
+    case 128:
+      if constexpr (D >= 128) return append_one<D, 128, ROT>(a, sm_count, stream, st);
+      break;
+    case 256:
+      if constexpr (D >= 256) return append_one<D, 256, ROT>(a, sm_count, stream, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <int D, int R, int NG>
@@ -192,16 +217,13 @@ cudaError_t launch_norm_rope(int dtype, const NormRopeArgs& args, int sm_count,
 }
 
 template <int D>
-cudaError_t launch_append(int dtype, int rot, int group, const AppendArgs& a, int sm_count,
+cudaError_t launch_append(int rot, int group, const AppendArgs& a, int sm_count,
                           cudaStream_t stream) {
   unsigned* st;
   cudaError_t e = detail::paged_status_ptr(&st);
   if (e != cudaSuccess) return e;
-  if (rot == kRotSRFT)
-    return dtype == kDtF16 ? detail::append_group<D, kRotSRFT, kDtF16>(a, group, sm_count, stream, st)
-                           : detail::append_group<D, kRotSRFT, kDtBF16>(a, group, sm_count, stream, st);
-  return dtype == kDtF16 ? detail::append_group<D, kRotSRHT, kDtF16>(a, group, sm_count, stream, st)
-                         : detail::append_group<D, kRotSRHT, kDtBF16>(a, group, sm_count, stream, st);
+  return rot == kRotSRFT ? detail::append_group<D, kRotSRFT>(a, group, sm_count, stream, st)
+                         : detail::append_group<D, kRotSRHT>(a, group, sm_count, stream, st);
 }
 
 template <int D>

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kvq_launch.h"
+
 namespace kvq {
 
 constexpr int kDtF16 = 0, kDtBF16 = 1;  // kvq_dtype
@@ -46,7 +48,7 @@ struct AppendArgs {
   const int8_t* signs;
   uint16_t *k_hat, *v_hat;  // NULL: not wanted
   int64_t n_tokens, n_slots;
-  int n_heads, page_shift;
+  int n_heads, page_shift, dtype;
 };
 
 struct PagedAttnArgs {
@@ -86,7 +88,7 @@ constexpr int64_t attn_workspace(int d, int64_t rows) {
 template <int D>
 cudaError_t launch_norm_rope(int dtype, const NormRopeArgs& a, int sm_count, cudaStream_t stream);
 template <int D>
-cudaError_t launch_append(int dtype, int rot, int group, const AppendArgs& a, int sm_count,
+cudaError_t launch_append(int rot, int group, const AppendArgs& a, int sm_count,
                           cudaStream_t stream);
 template <int D>
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int max_q_len, int sm_count,

@@ -11,8 +11,6 @@
 // Bound: bytes (2 d in, 2 d out per row).
 #pragma once
 
-#include <cuda_bf16.h>
-
 #include "kvq_device.cuh"
 #include "kvq_paged_launch.h"
 
@@ -32,8 +30,7 @@ __device__ __forceinline__ uint32_t float2_to_pair(float lo, float hi) {
   if constexpr (DT == kDtF16) {
     return float2_to_half2_bits(lo, hi);
   } else {
-    __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&b);
+    return float2_to_bf162_bits(lo, hi);
   }
 }
 

@@ -155,15 +155,16 @@ def _current(dev: torch.device):
     return torch.cuda.device(dev)
 
 
-def _on(stream, dev: torch.device):
-    """Context in which tensors allocated for a call belong to the stream the
-    call runs on: memory that the current stream's queued work still uses is
-    not handed to a kernel of another stream."""
+def _empty(like: torch.Tensor, shape, stream) -> torch.Tensor:
+    """An uninitialized tensor of `like`'s type and device that belongs to the
+    stream the call runs on: memory that the current stream's queued work still
+    uses is not handed to a kernel of another stream."""
     if stream is None:
-        return contextlib.nullcontext()
+        return like.new_empty(shape)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    return torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape)
 
 
 def _check(t: torch.Tensor, name: str, dtype, shape):
@@ -392,27 +393,34 @@ class PagedCache:
     d/group] f32, the sign vector [d] i8 and the rotation.  A page row is a row
     of kvq_rot_quant_fwd."""
 
+    __slots__ = ("k_packed", "k_scales", "v_packed", "v_scales", "signs", "rot", "n_pages",
+                 "n_kv_heads", "page_size", "d", "group", "device", "c", "ref")
+
     def __init__(self, k_packed: torch.Tensor, k_scales: torch.Tensor, v_packed: torch.Tensor,
                  v_scales: torch.Tensor, signs: torch.Tensor, rot: int = SRFT):
         if not isinstance(k_packed, torch.Tensor) or k_packed.dim() != 4:
             raise ValueError("k_packed must be a tensor [pages, heads, page_size, d/2]")
         if not isinstance(k_scales, torch.Tensor) or k_scales.dim() != 4 or k_scales.shape[3] < 1:
             raise ValueError("k_scales must be a tensor [pages, heads, page_size, d/group]")
-        self.n_pages, self.n_kv_heads, self.page_size, half = k_packed.shape
-        self.d = 2 * half
-        self.group = self.d // k_scales.shape[3]
-        self.rot = rot
-        for name, t in (("k_packed", k_packed), ("v_packed", v_packed)):
-            _check(t, name, torch.uint8, k_packed.shape)
-        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            _check(t, name, torch.float32, (*k_packed.shape[:3], self.d // max(self.group, 1)))
-        _check(signs, "signs", torch.int8, (self.d,))
+        pages, heads, page, half = shape = tuple(k_packed.shape)
+        d = 2 * half
+        group = d // k_scales.shape[3]
+        _check(k_packed, "k_packed", torch.uint8, shape)
+        _check(v_packed, "v_packed", torch.uint8, shape)
+        shape = (pages, heads, page, d // max(group, 1))
+        _check(k_scales, "k_scales", torch.float32, shape)
+        _check(v_scales, "v_scales", torch.float32, shape)
+        _check(signs, "signs", torch.int8, (d,))
+        self.device = _one_device((k_packed, k_scales, v_packed, v_scales, signs))
+        self.n_pages, self.n_kv_heads, self.page_size = pages, heads, page
+        self.d, self.group, self.rot = d, group, rot
         self.k_packed, self.k_scales = k_packed, k_scales
         self.v_packed, self.v_scales = v_packed, v_scales
         self.signs = signs
-        self.c = _PagedCacheC(_ptr(k_packed), _ptr(v_packed), _ptr(k_scales), _ptr(v_scales),
-                              self.n_pages, self.n_kv_heads, self.page_size, self.d, self.group,
-                              _ptr(signs), rot)
+        self.c = _PagedCacheC(k_packed.data_ptr(), v_packed.data_ptr(), k_scales.data_ptr(),
+                              v_scales.data_ptr(), pages, heads, page, d, group, signs.data_ptr(),
+                              rot)
+        self.ref = ctypes.addressof(self.c)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, d: int, group: int,
@@ -430,37 +438,77 @@ class PagedCache:
         return self.k_packed, self.k_scales, self.v_packed, self.v_scales, self.signs
 
 
+def _one_device(tensors) -> int:
+    """Index of the one CUDA device that every tensor (None: absent) lives on.
+    (Integer indexes: device objects cost a few hundred ns each to compare.)"""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if dev >= 0 or i < 0:
+                    _device_of(tensors, None)  # says which
+                    raise ValueError("all tensor arguments must be on one CUDA device")
+                dev = i
+    return dev
+
+
+def _enter(dev: int, stream):
+    """For a call on device index `dev`: (raw stream handle, context to leave).
+    The context is None when the device is current already."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, tensors on cuda:{dev}")
+    guard = None
+    if dev != torch.cuda.current_device():
+        guard = torch.cuda.device(dev)
+        guard.__enter__()
+    if stream is None:
+        if _raw_current_stream is not None:
+            return _raw_current_stream(dev), guard
+        stream = torch.cuda.current_stream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream), guard
+
+
+def _call(fn: str, dev: int, stream, args) -> None:
+    raw, guard = _enter(dev, stream)
+    try:
+        st = getattr(lib, fn)(*args, raw)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st != KVQ_OK:
+        raise KVQError(fn, st)
+
+
 def _check_tokens(t: torch.Tensor, name: str, dtype, shape) -> int:
     """Checks rows [tokens, heads, d] whose tokens may lie apart (a part of a
     fused projection); returns the token stride."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or dtype not in DTYPES:
+    if t.dtype is not dtype or dtype not in DTYPES:
         raise TypeError(f"{name} must be {dtype if dtype in DTYPES else 'float16 or bfloat16'}, "
                         f"got {t.dtype}")
-    if t.shape != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    heads, d = shape[1], shape[2]
-    if t.shape[0] <= 1:  # the stride of a single token says nothing
-        if heads * d and not (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)):
-            raise ValueError(f"the heads of a token of {name} must be contiguous")
-        return heads * d
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    tokens, heads, d = shape
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != d and heads > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0)
+    return st if tokens > 1 else heads * d  # the stride of a single token says nothing
 
 
 def _rope(positions, cos_sin, interleaved, eps, n_tokens):
-    rot_dim = n_pos = 0
-    if cos_sin is not None:
-        if positions is None:
-            raise ValueError("a rotation needs positions")
-        _check(positions, "positions", torch.int32, (n_tokens,))
-        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be a table [positions, rot_dim]")
-        _check(cos_sin, "cos_sin", torch.float32, cos_sin.shape)
-        n_pos, rot_dim = cos_sin.shape
-    return _RopeC(_ptr(cos_sin), n_pos, rot_dim, 1 if interleaved else 0, eps)
+    """(address of positions, kvq_rope) of a call."""
+    if cos_sin is None:
+        return None, _RopeC(None, 0, 0, 0, eps)
+    if positions is None:
+        raise ValueError("a rotation needs positions")
+    _check(positions, "positions", torch.int32, (n_tokens,))
+    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be a table [positions, rot_dim]")
+    n_pos, rot_dim = shape = cos_sin.shape
+    _check(cos_sin, "cos_sin", torch.float32, shape)
+    return positions.data_ptr(), _RopeC(cos_sin.data_ptr(), n_pos, rot_dim, bool(interleaved), eps)
 
 
 def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *,
@@ -474,32 +522,38 @@ def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *,
     table) of queries q [T, Hq, d] and keys k [T, Hk, d], fp16 or bf16, in one
     pass.  Returns (q_out, k_out), allocated when not given; they may be q and
     k themselves.  Rows of tokens at negative positions are left as they were."""
-    t, hq, d = q.shape
-    qs = _check_tokens(q, "q", q.dtype, (t, hq, d))
+    t, hq, d = shape = q.shape
+    dt = q.dtype
+    qs = _check_tokens(q, "q", dt, shape)
     if q_out is None:
-        with _on(stream, q.device):
-            q_out = torch.empty((t, hq, d), dtype=q.dtype, device=q.device)
-    qos = _check_tokens(q_out, "q_out", q.dtype, (t, hq, d))
+        q_out = _empty(q, shape, stream)
+        qos = hq * d
+    else:
+        qos = _check_tokens(q_out, "q_out", dt, shape)
     hk = ks = kos = 0
+    kp = kop = qwp = kwp = None
     if k is not None:
         hk = k.shape[1]
-        ks = _check_tokens(k, "k", q.dtype, (t, hk, d))
+        kshape = (t, hk, d)
+        ks = _check_tokens(k, "k", dt, kshape)
         if k_out is None:
-            with _on(stream, q.device):
-                k_out = torch.empty((t, hk, d), dtype=q.dtype, device=q.device)
-        kos = _check_tokens(k_out, "k_out", q.dtype, (t, hk, d))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check(w, name, torch.float32, (d,))
-    rope = _rope(positions, cos_sin, interleaved, eps, t)
-    dev = _device_of((q, k, positions if cos_sin is not None else None, cos_sin, q_weight,
-                      k_weight, q_out, k_out), stream)
-    with _current(dev):
-        st = lib.kvq_qk_norm_rope(_ptr(q), _ptr(k), DTYPES[q.dtype], t, hq, hk, d, qs, ks,
-                                  _ptr(positions), _ptr(q_weight), _ptr(k_weight),
-                                  ctypes.byref(rope), _ptr(q_out), _ptr(k_out), qos, kos,
-                                  _stream(stream, dev))
-    _raise("kvq_qk_norm_rope", st)
+            k_out = _empty(q, kshape, stream)
+            kos = hk * d
+        else:
+            kos = _check_tokens(k_out, "k_out", dt, kshape)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    if q_weight is not None:
+        _check(q_weight, "q_weight", torch.float32, (d,))
+        qwp = q_weight.data_ptr()
+    if k_weight is not None:
+        _check(k_weight, "k_weight", torch.float32, (d,))
+        kwp = k_weight.data_ptr()
+    pos, rope = _rope(positions, cos_sin, interleaved, eps, t)
+    dev = _one_device((q, k, positions if pos is not None else None, cos_sin, q_weight, k_weight,
+                       q_out, k_out))
+    _call("kvq_qk_norm_rope", dev, stream,
+          (q.data_ptr(), kp, DTYPES[dt], t, hq, hk, d, qs, ks, pos, qwp, kwp,
+           ctypes.addressof(rope), q_out.data_ptr(), kop, qos, kos))
     return q_out, k_out
 
 
@@ -513,25 +567,28 @@ def kvq_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cach
     cache, k after its norm and position rotation (as in kvq_qk_norm_rope).
     k_hat, v_hat [T, H, d], when given, receive the values the new rows stand
     for."""
+    dt = k.dtype
     t = k.shape[0]
     shape = (t, cache.n_kv_heads, cache.d)
-    ks = _check_tokens(k, "k", k.dtype, shape)
-    vs = _check_tokens(v, "v", k.dtype, shape)
+    ks = _check_tokens(k, "k", dt, shape)
+    vs = _check_tokens(v, "v", dt, shape)
     _check(slots, "slots", torch.int64, (t,))
+    kw = kh = vh = None
     if k_weight is not None:
         _check(k_weight, "k_weight", torch.float32, (cache.d,))
-    for name, x in (("k_hat", k_hat), ("v_hat", v_hat)):
-        if x is not None:
-            _check(x, name, k.dtype, shape)
-    rope = _rope(positions, cos_sin, interleaved, eps, t)
-    dev = _device_of((k, v, slots, positions if cos_sin is not None else None, cos_sin, k_weight,
-                      k_hat, v_hat, *cache.tensors()), stream)
-    with _current(dev):
-        st = lib.kvq_paged_append(_ptr(k), _ptr(v), DTYPES[k.dtype], t, ks, vs, _ptr(slots),
-                                  _ptr(positions), _ptr(k_weight), ctypes.byref(rope),
-                                  ctypes.byref(cache.c), _ptr(k_hat), _ptr(v_hat),
-                                  _stream(stream, dev))
-    _raise("kvq_paged_append", st)
+        kw = k_weight.data_ptr()
+    if k_hat is not None:
+        _check(k_hat, "k_hat", dt, shape)
+        kh = k_hat.data_ptr()
+    if v_hat is not None:
+        _check(v_hat, "v_hat", dt, shape)
+        vh = v_hat.data_ptr()
+    pos, rope = _rope(positions, cos_sin, interleaved, eps, t)
+    dev = _one_device((cache.signs, k, v, slots, positions if pos is not None else None, cos_sin,
+                       k_weight, k_hat, v_hat))
+    _call("kvq_paged_append", dev, stream,
+          (k.data_ptr(), v.data_ptr(), DTYPES[dt], t, ks, vs, slots.data_ptr(), pos, kw,
+           ctypes.addressof(rope), cache.ref, kh, vh))
 
 
 def kvq_paged_attend(q: torch.Tensor, cache: PagedCache, cu_q: torch.Tensor,
@@ -548,39 +605,37 @@ def kvq_paged_attend(q: torch.Tensor, cache: PagedCache, cu_q: torch.Tensor,
     sequence are left as they were.  The workspace (uint8) is allocated when
     not given; one that is given must not be used by another call before this
     one has finished on the device."""
-    t, h, d = q.shape
-    if d != cache.d or h % cache.n_kv_heads != 0 or h == 0:
+    t, h, d = shape = q.shape
+    dt = q.dtype
+    n_q = h // cache.n_kv_heads
+    if d != cache.d or n_q * cache.n_kv_heads != h or h == 0:
         raise ValueError(f"q [{t}, {h}, {d}] does not fit a cache of {cache.n_kv_heads} KV heads "
                          f"and d = {cache.d}")
-    qs = _check_tokens(q, "q", q.dtype, (t, h, d))
+    qs = _check_tokens(q, "q", dt, shape)
     if out is None:
-        with _on(stream, q.device):
-            out = torch.empty((t, h, d), dtype=q.dtype, device=q.device)
-    os_ = _check_tokens(out, "out", q.dtype, (t, h, d))
+        out = _empty(q, shape, stream)
+        outs = h * d
+    else:
+        outs = _check_tokens(out, "out", dt, shape)
     n_seqs = kv_len.shape[0]
+    max_pages = page_table.shape[-1]
     _check(kv_len, "kv_len", torch.int32, (n_seqs,))
     _check(cu_q, "cu_q", torch.int32, (n_seqs + 1,))
-    _check(page_table, "page_table", torch.int32, (n_seqs, page_table.shape[-1]))
-    scale = float(sm_scale) if sm_scale is not None else d ** -0.5
-    n_q = h // cache.n_kv_heads
-    if workspace is not None:
-        _check(workspace, "workspace", torch.uint8, (workspace.numel(),))
-    dev = _device_of((q, out, cu_q, kv_len, page_table, workspace, *cache.tensors()), stream)
-    with _current(dev):
-        if workspace is None:
-            need = lib.kvq_paged_attend_workspace(t, cache.n_kv_heads, n_q, d, max_q_len)
-            if need < 0:
-                _raise("kvq_paged_attend_workspace", -need)
-            if need > 0:
-                with _on(stream, dev):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = lib.kvq_paged_attend(_ptr(q), DTYPES[q.dtype], t, qs, ctypes.byref(cache.c),
-                                  _ptr(cu_q), _ptr(kv_len), _ptr(page_table), n_seqs,
-                                  page_table.shape[1], n_q, max_q_len, window, scale, _ptr(out),
-                                  os_, _ptr(workspace),
-                                  0 if workspace is None else workspace.numel(),
-                                  _stream(stream, dev))
-    _raise("kvq_paged_attend", st)
+    _check(page_table, "page_table", torch.int32, (n_seqs, max_pages))
+    if workspace is None:
+        need = lib.kvq_paged_attend_workspace(t, cache.n_kv_heads, n_q, d, max_q_len)
+        if need < 0:
+            raise KVQError("kvq_paged_attend_workspace", -need)
+        workspace = _empty(cache.k_packed, (need,), stream)
+    else:
+        need = workspace.numel()
+        _check(workspace, "workspace", torch.uint8, (need,))
+    dev = _one_device((cache.signs, q, out, cu_q, kv_len, page_table, workspace))
+    _call("kvq_paged_attend", dev, stream,
+          (q.data_ptr(), DTYPES[dt], t, qs, cache.ref, cu_q.data_ptr(), kv_len.data_ptr(),
+           page_table.data_ptr(), n_seqs, max_pages, n_q, max_q_len, window,
+           d ** -0.5 if sm_scale is None else float(sm_scale), out.data_ptr(), outs,
+           workspace.data_ptr(), need))
     return out
 
 

@@ -148,7 +148,9 @@ def check_append(kvq, cache, slots, values, hats, dtype):
                                      (256, 32), (256, 64), (256, 128), (256, 256)])
 @pytest.mark.parametrize("tokens,heads,page,norm,rot_dim,inter",
                          [(1, 1, 16, True, 64, False), (37, 3, 32, False, 0, False),
-                          (50, 2, 256, True, 32, True), (200, 5, 64, False, 48, False)])
+                          (50, 2, 256, True, 32, True), (200, 5, 64, False, 48, False),
+                          # enough rows for a thread a row; a last, partial tile
+                          (2601, 4, 64, True, 64, False), (5159, 2, 16, False, 32, True)])
 def test_append(kvq, dtype, rot, d, group, tokens, heads, page, norm, rot_dim, inter):
     g = gen(d + group + tokens)
     signs = torch.from_numpy(W.make_signs(d)).cuda()
@@ -180,6 +182,41 @@ def test_append(kvq, dtype, rot, d, group, tokens, heads, page, norm, rot_dim, i
         assert (t.transpose(1, 2).flatten(0, 1)[keep] == 0x5A).all()
     for t in (cache.k_scales, cache.v_scales):
         assert t.transpose(1, 2).flatten(0, 1)[keep].isnan().all()
+
+
+@pytest.mark.parametrize("d,group", [(64, 64), (128, 32), (256, 128)])
+def test_append_many_rows_skips_the_same(kvq, d, group):
+    """Padding, bad slots and bad positions among many rows: the rows written,
+    and their codes up to ties, are those of calls of few rows."""
+    t, h, page = 2601, 4, 32
+    signs = torch.from_numpy(W.make_signs(d)).cuda()
+    x = rows(gen(6), t, h, d, torch.float16)
+    slots = torch.randperm(t + 50, generator=gen(7), device="cuda")[:t]
+    slots[5], slots[40], slots[41], slots[2600] = -1, 10 ** 6, -(2 ** 40), 1 << 40
+    table = kvq.rope_table(3000, d // 2)
+    pos = torch.arange(t, device="cuda", dtype=torch.int32)
+    pos[77], pos[78] = 3000, -3
+    out = []
+    for parts in ([(0, t)], [(a, min(a + 100, t)) for a in range(0, t, 100)]):
+        cache = kvq.PagedCache.empty(t // page + 3, h, page, d, group, signs)
+        for c in cache.tensors()[:4]:
+            c.zero_()
+        hat = torch.full_like(x, 9.0)
+        for a, b in parts:
+            kvq.kvq_paged_append(x[a:b], x[a:b], slots[a:b], cache, positions=pos[a:b],
+                                 cos_sin=table, k_hat=hat[a:b])
+        assert kvq.kvq_device_status() == 11
+        out.append((cache, hat))
+    (c0, h0), (c1, h1) = out
+    skipped = [5, 40, 41, 77, 78, 2600]
+    assert (h0[skipped] == 9).all() and (h1[skipped] == 9).all()
+    assert torch.equal(h0 == 9, h1 == 9) or ((h0 == 9) != (h1 == 9)).float().mean() < 1e-3
+    for a, b in zip(c0.tensors()[:4], c1.tensors()[:4]):
+        if a.dtype == torch.uint8:
+            assert (a != b).float().mean() < 1e-3
+        else:
+            assert torch.equal(a > 0, b > 0) and ((a - b).abs() <= 4e-6 * b).all()
+    assert int((c0.v_scales > 0).any(-1).sum()) == (t - len(skipped)) * h
 
 
 def test_append_is_the_forward_step(kvq):
