@@ -77,8 +77,8 @@ struct PcShared {
   float ks[4][128], vs[4][128];  // by tile: K scales; V scales over 2^vexp
   int vexp[4];
   float wmax[2][4];
-  uint32_t sign_in[64], sign_out[64];  // d <= 128: sign masks of a row's words
-  int64_t scratch[16 + 4];
+  uint32_t sign_in[128], sign_out[128];  // sign masks of a row's words (of each thread of a pair)
+  int64_t scratch[kRunScratch];
 };
 
 // fp16 pairs of eight codes in the order 0 4 1 5 2 6 3 7.
@@ -151,41 +151,6 @@ __device__ __forceinline__ float pc_scale(float top, float qscale, float& back) 
   back = __uint_as_float(uint32_t(e - 8) << 23) * fabsf(qscale);  // 2^(e - 135)
   const float mul = __uint_as_float(uint32_t(262 - e) << 23);
   return qscale < 0.0f ? -mul : mul;
-}
-
-// Rotates one query row into the Q tile, a warp a row; returns (in every lane) the factor
-// from its products to log2 scores.
-template <int D, int ROT>
-__device__ __forceinline__ float pc_query(const PagedAttnArgs& a, const uint16_t* src, uint32_t tile,
-                                          int r, const WideLane<D, ROT>& L) {
-  using P = Wide<D, ROT>;
-  f2 z[P::C];
-#pragma unroll
-  for (int j = 0; j < P::C; ++j) {
-    const int w = ROT == kRotSRFT ? L.lane + 32 * j : P::C * L.lane + j;
-    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(src) + w) ^ L.mask[j];
-    const float2 f = a.dtype == kDtF16 ? pair_to_float2<kDtF16>(v) : pair_to_float2<kDtBF16>(v);
-    z[j] = mk2(f.x, f.y);
-  }
-  float Y[P::W];
-  wide_rotate_fwd<D, ROT>(z, L, Y);
-  float top = 0.0f;
-#pragma unroll
-  for (int w = 0; w < P::W; ++w) top = fmaxf(top, fabsf(Y[w]));
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  float back;
-  const float sg = pc_scale(top, a.qscale, back);
-#pragma unroll
-  for (int w = 0; w < P::W; ++w) {
-    const int c = pc_col(L.k2 * P::W + w);
-    const uint32_t at = tile + uint32_t(c >> 6) * 16384 + uint32_t(r) * 128 +
-                        ((uint32_t(c & 63) * 2) ^ (uint32_t(r & 7) << 4));
-    const __half h = __float2half_rn(Y[w] * sg);
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const uint16_t*>(&h))
-                 : "memory");
-  }
-  return back * P::KAPPA;
 }
 
 // d <= 128: a thread rotates its own row, in registers (the two-lane real FFT
@@ -274,6 +239,59 @@ __device__ __forceinline__ void pc_result_row(const PagedAttnArgs& a, f2 (&Y)[D 
   }
 }
 
+// d = 256: a lane pair rotates a row (every lane of the warp takes part; rows
+// that are not `there` read nothing).  The factor comes back in both lanes.
+template <int ROT>
+__device__ __forceinline__ float pc_query_pair(const PagedAttnArgs& a, const uint16_t* src,
+                                               bool there, uint32_t tile, int r, int t,
+                                               const uint32_t* sign) {
+  using C = Cfg<256, ROT, 2>;
+  f2 u[C::NW], Y[C::P];
+  const uint32_t* sg = sign + t * C::NW;
+  auto word = [&](uint32_t x, int j) {
+    x ^= sg[j];
+    const float2 f = a.dtype == kDtF16 ? pair_to_float2<kDtF16>(x) : pair_to_float2<kDtBF16>(x);
+    u[j] = mk2(f.x, f.y);
+  };
+  const uint4* p = reinterpret_cast<const uint4*>(src);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if constexpr (C::PAIR_RFFT) {  // half t of every word of the row, two to a word
+    const uint32_t sel = t ? 0x7632u : 0x5410u;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const uint4 v = there ? __ldg(p + c) : zero;
+      word(__byte_perm(v.x, v.y, sel), 2 * c);
+      word(__byte_perm(v.z, v.w, sel), 2 * c + 1);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const uint4 v = there ? __ldg(p + t * 16 + c) : zero;
+      word(v.x, 4 * c), word(v.y, 4 * c + 1), word(v.z, 4 * c + 2), word(v.w, 4 * c + 3);
+    }
+  }
+  rotate_fwd<C>(u, t, Y);
+  float top = absmax2<C::P>(Y);
+  top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+  float back;
+  const float mul = pc_scale(top, a.qscale, back);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // a quarter of the row: one 128-byte column
+    // (thread 1's second half of the Walsh-Hadamard pair is negated)
+    const float m = ROT == kRotSRHT && t == 1 && h == 1 ? -mul : mul;
+    const uint32_t at = tile + uint32_t(global_y<C>(t, 64 * h) >> 6) * 16384 + uint32_t(r) * 128;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const f2* y = Y + 32 * h + 4 * i;
+      sts128(at + (uint32_t((i ^ r) & 7) << 4), float2_to_half2_bits(lo2(y[0]) * m, lo2(y[2]) * m),
+             float2_to_half2_bits(hi2(y[0]) * m, hi2(y[2]) * m),
+             float2_to_half2_bits(lo2(y[1]) * m, lo2(y[3]) * m),
+             float2_to_half2_bits(hi2(y[1]) * m, hi2(y[3]) * m));
+    }
+  }
+  return back * C::KAPPA_INV;  // both ways the same
+}
+
 template <int D, int NG>
 __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
     kvq_paged_chunk_kernel(const PagedAttnArgs a, unsigned* status) {
@@ -305,13 +323,14 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
     fence_mbar_init();
   }
   pdl_wait();  // no global access before the previous kernel completes
-  if constexpr (D <= 128) {
-    if (tid < D / 2) {
-      sh.sign_in[tid] = a.rot == kRotSRFT ? load_mask_word<Cfg<D, kRotSRFT, 1>>(a.signs, 0, tid)
-                                          : load_mask_word<Cfg<D, kRotSRHT, 1>>(a.signs, 0, tid);
-      sh.sign_out[tid] = a.rot == kRotSRFT ? store_mask_word<Cfg<D, kRotSRFT, 1>>(a.signs, 0, tid)
-                                           : store_mask_word<Cfg<D, kRotSRHT, 1>>(a.signs, 0, tid);
-    }
+  if (tid < D / 2) {
+    using CF = Cfg<D, kRotSRFT, tpv_of(D)>;
+    using CH = Cfg<D, kRotSRHT, tpv_of(D)>;
+    const int t = tid / CF::NW, w = tid % CF::NW;
+    sh.sign_in[tid] = a.rot == kRotSRFT ? load_mask_word<CF>(a.signs, t, w)
+                                        : load_mask_word<CH>(a.signs, t, w);
+    sh.sign_out[tid] = a.rot == kRotSRFT ? store_mask_word<CF>(a.signs, t, w)
+                                         : store_mask_word<CH>(a.signs, t, w);
   }
   const Run run = find_run<M, KT, C::THREADS>(a, blockIdx.x, gridDim.x, sh.scratch, status);
   JoinInfo* join = a.join + blockIdx.x;
@@ -560,11 +579,13 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
             if (lane < nr)
               rowc = pc_query_row<D, ROT>(a, source(lane), qtile, w4 * 32 + lane, sh.sign_in);
           } else {
-            WideLane<D, ROT> L;
-            L.init(a.signs, lane);
-            for (int r = 0; r < nr; ++r) {
-              const float f = pc_query<D, ROT>(a, source(r), qtile, w4 * 32 + r, L);
-              if (lane == r) rowc = f;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {  // rows 0..15, then 16..31
+              const int r = 16 * h + lane / 2;
+              const float f = pc_query_pair<ROT>(a, source(min(r, max(nr - 1, 0))), r < nr, qtile,
+                                                 w4 * 32 + r, lane & 1, sh.sign_in);
+              const float g = __shfl_sync(kFull, f, 2 * (lane & 15));
+              if (lane >> 4 == h && lane < nr) rowc = g;
             }
           }
         };
@@ -592,8 +613,12 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
                            e.have == 0xFFu;
         const int hi = min(pos, e.len - 1) - e.t0;                     // last column seen
         const int lo = a.window > 0 ? pos - a.window + 1 - e.t0 : 0;   // first
-        auto seen = [&](int c) {
-          return c <= hi && c >= lo && (e.have >> (c >> 4) & 1u);
+        auto seen = [&](int c) {  // bit j: column c + j of 32 is seen
+          const int l = max(lo - c, 0), h = min(hi - c, 31);
+          const uint32_t there = e.have >> (c >> 4);
+          return h < l ? 0u
+                       : (0xFFFFFFFFu << l) & (0xFFFFFFFFu >> (31 - h)) &
+                             ((there & 1u ? 0xFFFFu : 0u) | (there & 2u ? 0xFFFF0000u : 0u));
         };
         const float4* ks4 = reinterpret_cast<const float4*>(sh.ks[i & 3]);
         const float4* vs4 = reinterpret_cast<const float4*>(sh.vs[i & 3]);
@@ -610,6 +635,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
             for (int c = 0; c < KT; c += 32) {
               uint32_t s[32];
               tmem_ld<32>(tS + c, s);
+              const uint32_t sm = MASK ? seen(c) : 0u;
               tmem_wait_ld();
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
@@ -617,8 +643,9 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
                 f2 u = mul2(mk2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), mk2(k.x, k.y));
                 f2 w = mul2(mk2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), mk2(k.z, k.w));
                 if constexpr (MASK) {
-                  u = mk2(seen(c + j) ? lo2(u) : -INFINITY, seen(c + j + 1) ? hi2(u) : -INFINITY);
-                  w = mk2(seen(c + j + 2) ? lo2(w) : -INFINITY, seen(c + j + 3) ? hi2(w) : -INFINITY);
+                  u = mk2(sm >> j & 1u ? lo2(u) : -INFINITY, sm >> (j + 1) & 1u ? hi2(u) : -INFINITY);
+                  w = mk2(sm >> (j + 2) & 1u ? lo2(w) : -INFINITY,
+                          sm >> (j + 3) & 1u ? hi2(w) : -INFINITY);
                 }
                 top = max3f(top, lo2(u), hi2(u));
                 top1 = max3f(top1, lo2(w), hi2(w));
@@ -664,6 +691,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
           for (int c = 0; c < KT; c += 32) {
             uint32_t s[32], p[16];
             tmem_ld<32>(tS + c, s);
+            const uint32_t sm = MASK ? seen(c) : 0u;
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
@@ -676,8 +704,8 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
                 const f2 z = fma2(t, rc2, nm2);
                 float z0 = lo2(z), z1 = hi2(z);
                 if constexpr (MASK) {
-                  if (!seen(c + j + b)) z0 = -INFINITY;
-                  if (!seen(c + j + b + 1)) z1 = -INFINITY;
+                  if (!(sm >> (j + b) & 1u)) z0 = -INFINITY;
+                  if (!(sm >> (j + b + 1) & 1u)) z1 = -INFINITY;
                 }
                 const f2 pp = mk2(ex2(z0), ex2(z1));
                 l2 = add2(l2, pp);
@@ -737,12 +765,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
             }
           }
         }
-        auto results = [&](auto rot) {
-          if constexpr (D <= 128) return;
-          constexpr int ROT = decltype(rot)::value;
-          WideLane<D, ROT> L;
-          L.init(a.signs, lane);
-          constexpr int W = D / 32;
+        if constexpr (D == 256) {
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {  // rows 0..15, then 16..31, through shared memory
             __syncwarp();
@@ -765,30 +788,61 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
               }
             }
             __syncwarp();
-#pragma unroll 1
-            for (int r = 0; r < 16 && h * 16 + r < nr; ++r) {
-              auto value = [&](int d) {
-                const int c = pc_col(d);
-                const uint32_t off = uint32_t(r) * (D * 4) +
-                                     ((uint32_t(c / 4) ^ uint32_t(r & 7)) << 4) + (c & 3) * 4;
-                return __uint_as_float(lds32(stage + (off >> 12) * 16384 + (off & 4095)));
-              };
-              const int g = r0 + h * 16 + r;
-              if (complete) {
-                float Y[W];
+            auto piece = [&](int r, int c4) {  // four columns of a row
+              const uint32_t off = uint32_t(r) * (D * 4) + ((uint32_t(c4) ^ uint32_t(r & 7)) << 4);
+              return lds128(stage + (off >> 12) * 16384 + (off & 4095));
+            };
+            if (complete) {  // a row a lane pair
+              auto rows_back = [&](auto rot) {
+                constexpr int ROT = decltype(rot)::value;
+                using C2 = Cfg<256, ROT, 2>;
+                const int r = lane >> 1, t = lane & 1;
+                f2 Y[C2::P];
+                const f2 kap = mk2(C2::KAPPA_INV, C2::KAPPA_INV);
 #pragma unroll
-                for (int w = 0; w < W; ++w) Y[w] = value(L.k2 * W + w) * Wide<D, ROT>::KAPPA;
-                pd_store<D, ROT>(a, Y, L, out_row(a, e.c0, e.head, e.row0 + g));
-              } else {
-                for (int d = lane; d < D; d += 32) slot[2 * M + g * D + d] = value(d);
+                for (int q = 0; q < 2; ++q) {
+                  const int c0 = global_y<C2>(t, 64 * q) / 4;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {  // columns 0 4 1 5, 2 6 3 7
+                    const uint4 v = piece(r, c0 + 2 * i), w = piece(r, c0 + 2 * i + 1);
+                    auto pair = [&](uint32_t x, uint32_t y) {
+                      return mul2(mk2(__uint_as_float(x), __uint_as_float(y)), kap);
+                    };
+                    f2* y = Y + 32 * q + 4 * i;
+                    y[0] = pair(v.x, v.z), y[1] = pair(w.x, w.z);
+                    y[2] = pair(v.y, v.w), y[3] = pair(w.y, w.w);
+                  }
+                }
+                uint32_t xw[C2::NW];
+                rotate_inv<C2>(Y, t, xw, 0, a.dtype == kDtBF16);
+                if (16 * h + r < nr) {
+                  uint4* dst = reinterpret_cast<uint4*>(
+                                   out_row(a, e.c0, e.head, e.row0 + r0 + 16 * h + r)) + t * 16;
+                  const uint32_t* m = sh.sign_out + t * C2::NW;
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    dst[j] = make_uint4(xw[4 * j] ^ m[4 * j], xw[4 * j + 1] ^ m[4 * j + 1],
+                                        xw[4 * j + 2] ^ m[4 * j + 2], xw[4 * j + 3] ^ m[4 * j + 3]);
+                }
+              };
+              if (a.rot == kRotSRFT)
+                rows_back(std::integral_constant<int, kRotSRFT>{});
+              else
+                rows_back(std::integral_constant<int, kRotSRHT>{});
+            } else {
+#pragma unroll 1
+              for (int r = 0; r < 16 && h * 16 + r < nr; ++r) {
+                float* to = slot + 2 * M + (r0 + h * 16 + r) * D;
+                for (int d = lane; d < D; d += 32) {
+                  const int c = pc_col(d);
+                  const uint4 v = piece(r, c >> 2);
+                  const uint32_t x = (c & 2) ? ((c & 1) ? v.w : v.z) : ((c & 1) ? v.y : v.x);
+                  to[d] = __uint_as_float(x);
+                }
               }
             }
           }
-        };
-        if (a.rot == kRotSRFT)
-          results(std::integral_constant<int, kRotSRFT>{});
-        else
-          results(std::integral_constant<int, kRotSRHT>{});
+        }
         if (e.last && !began_here && tid == 0) {
           join->c0 = e.c0;
           join->head = e.head;

@@ -120,7 +120,7 @@ struct PdShared {
   float f[4][16], icw[4][16], m[4][16], l[4][4][16];  // by tile
   float fcur[16], icwcur[16], mcur[16];
   float red[4][16], red2[4][16];
-  int64_t scratch[kPdThreads / 32 + 4];
+  int64_t scratch[kRunScratch];
 };
 
 // smem byte of coordinate i (0..D) of a token, before the 128-byte column is

@@ -27,39 +27,52 @@ __device__ __forceinline__ SeqInfo load_seq(const PagedAttnArgs& a, int s, unsig
   return SeqInfo{b, e - b, len};
 }
 
-// Tiles of cached rows of row tile qt: first tile and their number.
+// Tiles of cached rows of row tile qt: first tile and their number.  (32-bit
+// arithmetic: rows, positions and lengths are below 2^31.)
 template <int M, int KT>
 __device__ __forceinline__ void item_tiles(const PagedAttnArgs& a, const SeqInfo& q, int qt,
                                            int& first, int& count) {
-  const int last_row = min(int64_t(q.n) * a.n_q, (int64_t(qt) + 1) * M) - 1;
-  const int64_t p0 = int64_t(q.len) - q.n + int64_t(qt) * M / a.n_q;
-  const int64_t hi = int64_t(q.len) - q.n + last_row / a.n_q + 1;
-  const int64_t lo = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
+  const unsigned row = unsigned(qt) * M, rows = unsigned(q.n) * unsigned(a.n_q);
+  const unsigned last = min(rows, row + M) - 1;
+  const int p0 = q.len - q.n + int(row / unsigned(a.n_q));
+  const int hi = q.len - q.n + int(last / unsigned(a.n_q)) + 1;
+  const int lo = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
   if (hi <= lo) {
     first = 0;
     count = 1;
   } else {
-    first = int(lo / KT);
-    count = int((hi + KT - 1) / KT) - first;
+    first = int(unsigned(lo) / KT);
+    count = int((unsigned(hi) + KT - 1) / KT) - first;
   }
 }
 
 template <int M>
 __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, const SeqInfo& q) {
-  return int((int64_t(q.n) * a.n_q + M - 1) / M);
+  return int((unsigned(q.n) * unsigned(a.n_q) + M - 1) / M);
 }
 
-// Units of one head of a sequence.
-template <int M, int KT>
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {  // inclusive, over the lanes
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(kFull, x, o);
+    if ((threadIdx.x & 31) >= o) x += up;
+  }
+  return x;
+}
+
+// Units of one head of a sequence, summed by the lanes of a warp (the same
+// sequence in all) or by one thread.
+template <int M, int KT, bool WARP>
 __device__ __forceinline__ int64_t head_units(const PagedAttnArgs& a, const SeqInfo& q) {
   int64_t u = 0;
   const int nqt = row_tiles<M>(a, q);
-  for (int qt = 0; qt < nqt; ++qt) {
+#pragma unroll 1
+  for (int qt = WARP ? threadIdx.x & 31 : 0; qt < nqt; qt += WARP ? 32 : 1) {
     int f, c;
     item_tiles<M, KT>(a, q, qt, f, c);
     u += c;
   }
-  return u;
+  return WARP ? __shfl_sync(kFull, warp_scan(u), 31) : u;
 }
 
 // A place in the order of units.
@@ -86,19 +99,36 @@ struct Cursor {
     }
     item(a);
   }
+  // To unit `off` of sequence s; by a whole warp.
   __device__ __forceinline__ void seek(const PagedAttnArgs& a, int s, int64_t off) {
     seq = s;
     q = load_seq(a, s, nullptr);
     nqt = row_tiles<M>(a, q);
-    const int64_t per_head = head_units<M, KT>(a, q);
+    if (nqt == 1) {
+      qt = 0;
+      item(a);
+      head = int(off / count);
+      tile = int(off - int64_t(head) * count);
+      return;
+    }
+    const int64_t per_head = head_units<M, KT, true>(a, q);
     head = int(off / per_head);
     off -= head * per_head;
-    for (qt = 0;; ++qt) {
-      item(a);
-      if (off < count) break;
-      off -= count;
+    const int lane = threadIdx.x & 31;
+    for (int base = 0;; base += 32) {  // the lanes count 32 row tiles at a time
+      int f = 0, c = 0;
+      if (base + lane < nqt) item_tiles<M, KT>(a, q, base + lane, f, c);
+      const int64_t end = warp_scan(c);
+      const uint32_t past = __ballot_sync(kFull, end > off);
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        qt = base + l;
+        tile = int(off - __shfl_sync(kFull, end - c, l));
+        item(a);
+        return;
+      }
+      off -= __shfl_sync(kFull, end, 31);
     }
-    tile = int(off);
   }
 };
 
@@ -109,25 +139,49 @@ struct Run {
   int64_t off;                // units of that sequence before it
 };
 
-// The run of block b of `blocks`; called by all NT threads, `s` scratch for
-// NT / 32 + 4 values.
+constexpr int kFewSeqs = 64;  // up to here a warp counts a sequence, above a thread
+constexpr int kRunScratch = kFewSeqs + 4;
+
+// The run of block b of `blocks`; called by all NT threads, `s` scratch.
 template <int M, int KT, int NT>
-__device__ __forceinline__ Run find_run(const PagedAttnArgs& a, int b, int blocks, int64_t* s,
-                                        unsigned* status) {
+__device__ __forceinline__ Run find_run(const PagedAttnArgs& a, int b, int blocks,
+                                        int64_t (&s)[kRunScratch], unsigned* status) {
+  static_assert(NT / 32 <= kFewSeqs, "scratch");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned* st = b == 0 ? status : nullptr;
+  Run r{0, 0, 0, 0, 0, 0};
+  auto cut = [&]() {
+    r.blocks = int(min(int64_t(blocks), r.total));
+    if (b >= r.blocks) return false;
+    r.begin = r.total * b / r.blocks;
+    r.end = r.total * (b + 1) / r.blocks;
+    return true;
+  };
+  if (a.n_seqs <= kFewSeqs) {
+#pragma unroll 1
+    for (int sq = warp; sq < a.n_seqs; sq += NT / 32) {
+      const SeqInfo q = load_seq(a, sq, lane == 0 ? st : nullptr);
+      const int64_t u = q.n > 0 ? head_units<M, KT, true>(a, q) * a.n_kv : 0;
+      if (lane == 0) s[sq] = u;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < a.n_seqs; ++i) r.total += s[i];
+    if (!cut()) return r;
+    int64_t before = 0;
+#pragma unroll 1
+    for (r.seq = 0; before + s[r.seq] <= r.begin; ++r.seq) before += s[r.seq];
+    r.off = r.begin - before;
+    return r;
+  }
   auto scan = [&](int base, int64_t& mine, int64_t& incl) {  // units of seqs base + tid
     const int sq = base + tid;
     mine = 0;
     if (sq < a.n_seqs) {
-      const SeqInfo q = load_seq(a, sq, b == 0 ? status : nullptr);
-      if (q.n > 0) mine = head_units<M, KT>(a, q) * a.n_kv;
+      const SeqInfo q = load_seq(a, sq, st);
+      if (q.n > 0) mine = head_units<M, KT, false>(a, q) * a.n_kv;
     }
-    incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += up;
-    }
+    incl = warp_scan(mine);
     __syncthreads();  // the scratch of the call before is read
     if (lane == 31) s[warp] = incl;
     __syncthreads();
@@ -138,13 +192,9 @@ __device__ __forceinline__ Run find_run(const PagedAttnArgs& a, int b, int block
     for (int w = 0; w < NT / 32; ++w) all += s[w];
     return all;
   };
-  Run r{0, 0, 0, 0, 0, 0};
   int64_t mine, incl;
   for (int base = 0; base < a.n_seqs; base += NT) r.total += scan(base, mine, incl);
-  r.blocks = int(min(int64_t(blocks), r.total));
-  if (b >= r.blocks) return r;
-  r.begin = r.total * b / r.blocks;
-  r.end = r.total * (b + 1) / r.blocks;
+  if (!cut()) return r;
   int64_t before = 0;
   for (int base = 0; base < a.n_seqs; base += NT) {
     // one chunk: the scan above still holds
@@ -152,16 +202,16 @@ __device__ __forceinline__ Run find_run(const PagedAttnArgs& a, int b, int block
     if (r.begin < before + all) {
       const int64_t end = before + incl, start = end - mine;
       if (start <= r.begin && r.begin < end) {
-        s[NT / 32] = base + tid;
-        s[NT / 32 + 1] = r.begin - start;
+        s[kFewSeqs] = base + tid;
+        s[kFewSeqs + 1] = r.begin - start;
       }
       break;
     }
     before += all;
   }
   __syncthreads();
-  r.seq = int(s[NT / 32]);
-  r.off = s[NT / 32 + 1];
+  r.seq = int(s[kFewSeqs]);
+  r.off = s[kFewSeqs + 1];
   return r;
 }
 

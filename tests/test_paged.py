@@ -415,6 +415,7 @@ def test_attend_one_token(kvq, dtype, rot, d, group, nq, heads, page, lens):
 
 
 @pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("rot", [O.SRFT, O.SRHT])
 @pytest.mark.parametrize("d,group", SHAPES)
 @pytest.mark.parametrize("nq,heads,page,news,lens,window", [
     (1, 2, 16, [5, 1, 3], [5, 40, 130], 0),          # drafted tokens, one from position 0
@@ -422,8 +423,8 @@ def test_attend_one_token(kvq, dtype, rot, d, group, nq, heads, page, lens):
     (4, 1, 64, [70, 33], [333, 33], 50),             # a sliding window
     (3, 2, 16, [100], [257], 1),                     # each token sees itself alone
     (16, 1, 16, [9], [140], 0)])
-def test_attend_chunk(kvq, dtype, d, group, nq, heads, page, news, lens, window):
-    cache = make_pool(kvq, d + nq, sum(-(-m // page) for m in lens) + 2, heads, page, d, group, 0)
+def test_attend_chunk(kvq, dtype, rot, d, group, nq, heads, page, news, lens, window):
+    cache = make_pool(kvq, d + nq, sum(-(-m // page) for m in lens) + 2, heads, page, d, group, rot)
     table = make_batch(cache, 6, lens)
     poison(cache, table, lens)
     cu = np.concatenate([[0], np.cumsum(news)]).tolist()
