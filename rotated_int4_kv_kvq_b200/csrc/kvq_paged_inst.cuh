@@ -41,10 +41,10 @@ inline cudaError_t paged_status_ptr(unsigned** out) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_paged(void (*kern)(KArgs...), int64_t grid, int threads, int smem,
-                         cudaStream_t stream, Args&&... args) {
+cudaError_t launch_paged_2d(void (*kern)(KArgs...), int64_t grid, int rows, int threads, int smem,
+                            cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(grid), 1, 1);
+  cfg.gridDim = dim3(unsigned(grid), unsigned(rows), 1);
   cfg.blockDim = dim3(unsigned(threads), 1, 1);
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = stream;
@@ -55,6 +55,12 @@ cudaError_t launch_paged(void (*kern)(KArgs...), int64_t grid, int threads, int 
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
   return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_paged(void (*kern)(KArgs...), int64_t grid, int threads, int smem,
+                         cudaStream_t stream, Args&&... args) {
+  return launch_paged_2d(kern, grid, 1, threads, smem, stream, std::forward<Args>(args)...);
 }
 
 // Opts a kernel into its shared memory (once per kernel and device).
@@ -120,6 +126,14 @@ cudaError_t append_group(const AppendArgs& a, int group, int sm_count, cudaStrea
   return cudaErrorInvalidValue;
 }
 
+template <int D, int R, int RPB, int WPR>
+cudaError_t launch_join(const PagedAttnArgs& a, int64_t grid, cudaStream_t stream) {
+  return a.rot == kRotSRFT ? launch_paged_2d(kvq_paged_join_kernel<D, R, kRotSRFT, RPB, WPR>, grid,
+                                             R / RPB, 32 * RPB * WPR, 0, stream, a)
+                           : launch_paged_2d(kvq_paged_join_kernel<D, R, kRotSRHT, RPB, WPR>, grid,
+                                             R / RPB, 32 * RPB * WPR, 0, stream, a);
+}
+
 template <int D, int R, int NG>
 cudaError_t few_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t stream, unsigned* st) {
   using C = Pd<D, R, NG>;
@@ -137,9 +151,7 @@ cudaError_t few_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t strea
   a.parts = reinterpret_cast<float*>(a.workspace + kMaxBlocks * 32);
   e = launch_paged(kern, grid, kPdThreads, C::SMEM, stream, a, st);
   if (e != cudaSuccess) return e;
-  return a.rot == kRotSRFT
-             ? launch_paged(kvq_paged_join_kernel<D, R, kRotSRFT>, grid, 256, 0, stream, a)
-             : launch_paged(kvq_paged_join_kernel<D, R, kRotSRHT>, grid, 256, 0, stream, a);
+  return launch_join<D, R, 4, 4>(a, grid, stream);
 }
 
 template <int D, int NG>
@@ -158,9 +170,7 @@ cudaError_t many_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t stre
   a.parts = reinterpret_cast<float*>(a.workspace + kMaxBlocks * 32);
   e = launch_paged(kern, grid, C::THREADS, C::SMEM, stream, a, st);
   if (e != cudaSuccess) return e;
-  return a.rot == kRotSRFT
-             ? launch_paged(kvq_paged_join_kernel<D, C::M, kRotSRFT>, grid, 256, 0, stream, a)
-             : launch_paged(kvq_paged_join_kernel<D, C::M, kRotSRHT>, grid, 256, 0, stream, a);
+  return launch_join<D, C::M, 8, 1>(a, grid, stream);
 }
 
 template <int D>

@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < kPcRing; ++i) {
       mbar_init(bar(sh.dfull[i]), 1);
-      mbar_init(bar(sh.dfree[i]), NT * 4);
+      mbar_init(bar(sh.dfree[i]), NT * 4 + 1);  // the softmax, and the MMA warp
     }
     for (int i = 0; i < 4; ++i) mbar_init(bar(sh.scfull[i]), 4);
     for (int i = 0; i < 2; ++i) {
@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
   const Run run = find_run<M, KT, C::THREADS>(a, blockIdx.x, gridDim.x, sh.scratch, status);
   JoinInfo* join = a.join + blockIdx.x;
   if (tid == 0) join->first_block = -1;
+  pdl_release();  // the join's blocks wait for this grid's end: let them be placed
   if (run.begin == run.end) return;
   const int n = int(run.end - run.begin);  // tiles
   if (warp == C::W_MMA) tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -434,8 +435,12 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
     for (int i = 0; i < n; ++i) {
       wait(sh.dfull[i % kPcRing], i / kPcRing);
       const bool starts = sh.tiles[i % kPcRing].starts, ends = sh.tiles[i % kPcRing].ends;
+      const int rows = sh.tiles[i % kPcRing].rows;
+      // (this tile's scores are under way, so the softmax may be through with the
+      // description before it is read here)
+      arrive(sh.dfree[i % kPcRing]);
       if (starts) {
-        two = NT == 2 && sh.tiles[i % kPcRing].rows > 128;
+        two = NT == 2 && rows > 128;
         wait(sh.qfull[0], items[0]++);
         if (two) wait(sh.qfull[1], items[1]++);
         wait(sh.kfull[i % KS], i / KS);
@@ -856,7 +861,6 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
     }
   }
   if (!ok && lane == 0) atomicOr(status, kPagedTimeout);
-  pdl_release();
   tc_fence_before();
   __syncthreads();  // every use of tensor memory is over
   if (warp == C::W_MMA) tmem_free(tmem, 512);

@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
   const Run run = find_run<R, KT, kPdThreads>(a, blockIdx.x, gridDim.x, sh.scratch, status);
   JoinInfo* join = a.join + blockIdx.x;
   if (tid == 0) join->first_block = -1;
+  pdl_release();  // the join's blocks wait for this grid's end: let them be placed
   if (run.begin == run.end) return;
   const int n = int(run.end - run.begin);  // tiles
   if (warp == 12) tmem_alloc(smem_u32(&sh.tmem), C::TMEM);
@@ -809,45 +810,62 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     }
   }
   if (!ok && lane == 0) atomicOr(status, kPagedTimeout);
-  pdl_release();
   tc_fence_before();
   __syncthreads();  // every read of tensor memory is done
   if (warp == 12) tmem_free(tmem, C::TMEM);
 }
 
-// Joins the partial results of items that several blocks shared: block b the
-// one that ended in block b, a warp a row.
-template <int D, int R, int ROT>
-__global__ void __launch_bounds__(256) kvq_paged_join_kernel(const PagedAttnArgs a) {
-  pdl_wait();  // the partial results of the kernel before
-  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const JoinInfo j = a.join[b];
-  if (j.first_block < 0) return;
-  WideLane<D, ROT> L;
-  L.init(a.signs, lane);
+// Joins the partial results of items that several blocks shared: blockIdx.x the
+// one that ended in that block, blockIdx.y a run of RPB rows of it, WPR warps a
+// row (each takes every WPR-th part, eight in flight; an item of few rows over a
+// long sequence has as many parts as there are blocks).
+template <int D, int R, int ROT, int RPB, int WPR>
+__global__ void __launch_bounds__(32 * RPB * WPR) kvq_paged_join_kernel(const PagedAttnArgs a) {
   constexpr int W = D / 32;
-  for (int r = warp; r < j.rows; r += 8) {
-    float top = -3e38f;
+  __shared__ float s_part[WPR > 1 ? RPB * WPR : 1][D + 2];
+  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * RPB + warp / WPR, share = warp % WPR;
+  WideLane<D, ROT> L;
+  L.init(a.signs, lane);  // (signs are no kernel's output)
+  pdl_wait();             // the partial results of the kernel before
+  const JoinInfo j = a.join[b];
+  if (j.first_block < 0 || int(blockIdx.y) * RPB >= j.rows) return;
+  const bool there = r < j.rows;
+  float Y[W], l = 0.0f, top = -3e38f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) Y[w] = 0.0f;
+  if (there) {
     for (int p = j.first_block + lane; p <= b; p += 32)
       top = fmaxf(top, part_slot<D, R>(a, p, p == j.first_block ? 1 : 0)[r]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    float Y[W], l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) Y[w] = 0.0f;
-#pragma unroll 4
-    for (int p = j.first_block; p <= b; ++p) {
+#pragma unroll 8
+    for (int p = j.first_block + share; p <= b; p += WPR) {
       const float* slot = part_slot<D, R>(a, p, p == j.first_block ? 1 : 0);
-      const float f = exp2f(slot[r] - top);
+      const float f = ex2(slot[r] - top);
       l = fmaf(f, slot[R + r], l);
 #pragma unroll
       for (int w = 0; w < W; ++w) Y[w] = fmaf(f, slot[2 * R + r * D + L.k2 * W + w], Y[w]);
     }
-    const float inv = l > 0.0f ? Wide<D, ROT>::KAPPA / l : 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) Y[w] *= inv;
-    pd_store<D, ROT>(a, Y, L, out_row(a, j.c0, j.head, j.row0 + r));
   }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) s_part[warp][L.k2 * W + w] = Y[w];
+    if (lane == 0) s_part[warp][D] = l;
+    __syncthreads();
+    if (share != 0) return;
+#pragma unroll
+    for (int x = 1; x < WPR; ++x) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) Y[w] += s_part[warp + x][L.k2 * W + w];
+      l += s_part[warp + x][D];
+    }
+  }
+  if (!there) return;
+  const float inv = l > 0.0f ? Wide<D, ROT>::KAPPA / l : 0.0f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) Y[w] *= inv;
+  pd_store<D, ROT>(a, Y, L, out_row(a, j.c0, j.head, j.row0 + r));
 }
 
 }  // namespace kvq

@@ -617,6 +617,26 @@ def test_attend_chunk_long(kvq, dtype, d, group, nq, heads, page, news, lens, wi
     check_large(kvq, cache, q, cu, lens, table, window)
 
 
+@pytest.mark.parametrize("d,group,nq,new", [(256, 256, 6, 5), (256, 256, 8, 16), (128, 32, 8, 16),
+                                            (64, 64, 4, 40), (128, 128, 4, 1), (64, 64, 1, 1)])
+def test_attend_repeats(kvq, d, group, nq, new):
+    """The same call many times over, runs of many tiles and items in every
+    block: the roles of a block meet in ever other orders, the result stays."""
+    seqs, length, heads, page = 32, 3000, 8, 32
+    cache = make_pool(kvq, d, seqs * 94, heads, page, d, group, 0)
+    table = make_batch(cache, 21, [length] * seqs)
+    q = rows(gen(22), seqs * new, heads * nq, d, torch.float16) * 0.25
+    dev = dict(device="cuda", dtype=torch.int32)
+    cu = torch.arange(seqs + 1, **dev) * new
+    lens = torch.full((seqs,), length, **dev)
+    first = kvq.kvq_paged_attend(q, cache, cu, lens, table, max_q_len=new)
+    out = torch.empty_like(first)
+    for i in range(500):
+        kvq.kvq_paged_attend(q, cache, cu, lens, table, max_q_len=new, out=out)
+        if i % 100 == 99:
+            assert kvq.kvq_device_status() == 0 and torch.equal(out, first)
+
+
 def test_attend_many_sequences(kvq):
     """More sequences than threads of a block, most of them idle."""
     n = 1500
