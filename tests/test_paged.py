@@ -679,3 +679,133 @@ def test_steps_of_a_layer(kvq, dtype, d, group, nq, window):
         want = O.norm_rope(np64(k), np64(kw), pos.tolist(), rope.cpu().numpy())
         check_append(kvq, cache, slots, (want, np64(v)), (None, None), dtype)
         run_attend(kvq, cache, q, [0, news[0], n], lens, table, window=window)
+
+
+# ----------------------------------------------------- streams, graphs, devices ---
+
+def layer_state(kvq, d, group, news, seed, dtype=torch.float16):
+    """A batch in flight: cache with history, new tokens, tables."""
+    heads, nq, page = 2, 4, 16
+    signs = torch.from_numpy(W.make_signs(d)).cuda()
+    cache = make_pool(kvq, seed, 40, heads, page, d, group, 0)
+    lens = [150 + n for n in news]
+    table = torch.randperm(40, generator=gen(seed), device="cuda").to(torch.int32).reshape(2, 20)
+    n = sum(news)
+    qkv = rows(gen(seed + 1), n, heads * (nq + 2), d, dtype)
+    dev = dict(device="cuda", dtype=torch.int32)
+    cu, ln = torch.tensor([0, news[0], n], **dev), torch.tensor(lens, **dev)
+    pos, slots = kvq.paged_rows(cu, ln, table, page, n)
+    return dict(cache=cache, qkv=qkv, cu=cu, ln=ln, table=table, pos=pos, slots=slots,
+                rope=kvq.rope_table(400, d), most=max(news), nq=heads * nq, heads=heads,
+                w=1 + 0.1 * torch.randn(d, generator=gen(seed + 2), device="cuda"))
+
+
+def layer(kvq, s, stream=None):
+    q, k, v = s["qkv"].split([s["nq"], s["heads"], s["heads"]], 1)
+    kvq.kvq_paged_append(k, v, s["slots"], s["cache"], positions=s["pos"], cos_sin=s["rope"],
+                         k_weight=s["w"], stream=stream)
+    q, _ = kvq.kvq_qk_norm_rope(q, positions=s["pos"], cos_sin=s["rope"], q_weight=s["w"],
+                                stream=stream)
+    return kvq.kvq_paged_attend(q, s["cache"], s["cu"], s["ln"], s["table"], max_q_len=s["most"],
+                                stream=stream)
+
+
+LAYERS = [(64, 64, [1, 1]), (128, 32, [3, 1]), (256, 256, [40, 7]), (128, 128, [90, 60])]
+
+
+@pytest.mark.parametrize("d,group,news", LAYERS)
+def test_captured_layer_replays(kvq, d, group, news):
+    """A layer captured into a graph follows what its inputs hold at each
+    replay: other tokens, other lengths, other pages."""
+    s, other = layer_state(kvq, d, group, news, 3), layer_state(kvq, d, group, news, 4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        out = layer(kvq, s)
+    torch.cuda.current_stream().wait_stream(side)
+    for x in (s, other):
+        # (the graph's inputs take x's values; x itself is computed eagerly on copies)
+        eager = dict(x, cache=kvq.PagedCache(*(t.clone() for t in x["cache"].tensors()), 0))
+        want = layer(kvq, eager)
+        if x is other:
+            for name in ("qkv", "cu", "ln", "table", "pos", "slots", "w"):
+                s[name].copy_(x[name])
+            for a, b in zip(s["cache"].tensors(), x["cache"].tensors()):
+                a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        for a, b in zip(s["cache"].tensors(), eager["cache"].tensors()):
+            assert torch.equal(a, b)
+    assert kvq.kvq_device_status() == 0
+    del graph
+
+
+def test_two_streams_at_once(kvq):
+    """Calls of different shapes on two streams, each its own workspace: the
+    results are those of calls one after the other."""
+    states = [layer_state(kvq, d, g, n, 10 + i) for i, (d, g, n) in enumerate(LAYERS)]
+    want = [layer(kvq, s) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    for _ in range(20):
+        got = [layer(kvq, s, stream=st) for s, st in zip(states, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert kvq.kvq_device_status() == 0
+    # a raw handle, and a stream that is current
+    got = layer(kvq, states[1], stream=streams[0].cuda_stream)
+    streams[0].synchronize()
+    assert torch.equal(got, want[1])
+    with torch.cuda.stream(streams[2]):
+        got = layer(kvq, states[2])
+    streams[2].synchronize()
+    assert torch.equal(got, want[2])
+
+
+def test_own_workspace_and_refusals(kvq):
+    s = layer_state(kvq, 128, 32, [3, 1], 5)
+    want = layer(kvq, s)
+    q, k, v = s["qkv"].split([s["nq"], s["heads"], s["heads"]], 1)
+    q, _ = kvq.kvq_qk_norm_rope(q, positions=s["pos"], cos_sin=s["rope"], q_weight=s["w"])
+    need = kvq.lib.kvq_paged_attend_workspace(q.shape[0], s["heads"], 4, 128, s["most"])
+    args = (q, s["cache"], s["cu"], s["ln"], s["table"])
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")  # holds no meaning before
+    assert torch.equal(kvq.kvq_paged_attend(*args, max_q_len=s["most"], workspace=ws), want)
+    with pytest.raises(kvq.KVQError, match="BAD_SIZE"):
+        kvq.kvq_paged_attend(*args, max_q_len=s["most"], workspace=ws[:-256])
+    with pytest.raises(kvq.KVQError, match="MISALIGNED"):
+        kvq.kvq_paged_attend(*args, max_q_len=s["most"], workspace=torch.cat([ws, ws])[16:])
+    with pytest.raises(ValueError, match="does not fit"):
+        kvq.kvq_paged_attend(q[:, :7], *args[1:], max_q_len=1)
+    with pytest.raises(ValueError, match="contiguous"):
+        kvq.kvq_paged_attend(q[..., ::2].repeat(1, 1, 2)[:, ::2], *args[1:], max_q_len=1)
+    with pytest.raises(TypeError, match="float16 or bfloat16"):
+        kvq.kvq_paged_attend(q.float(), *args[1:], max_q_len=1)
+    with pytest.raises(TypeError, match="int32"):
+        kvq.kvq_paged_attend(q, s["cache"], s["cu"].long(), *args[3:], max_q_len=1)
+    with pytest.raises(ValueError, match="positions"):
+        kvq.kvq_qk_norm_rope(q, cos_sin=s["rope"])
+    with pytest.raises(TypeError, match="bfloat16"):
+        kvq.kvq_paged_append(k.bfloat16(), v, s["slots"], s["cache"])
+    with pytest.raises(kvq.KVQError, match="MISALIGNED"):
+        wide = torch.zeros((4, 9 * 128 + 8), dtype=torch.float16, device="cuda")
+        kvq.kvq_qk_norm_rope(wide[:, 4:4 + 8 * 128].unflatten(1, (8, 128)))
+    with pytest.raises(kvq.KVQError, match="BAD_SIZE"):  # a token stride that is no multiple of 8
+        wide = torch.zeros((4, 8 * 128 + 4), dtype=torch.float16, device="cuda")
+        kvq.kvq_qk_norm_rope(wide[:, :8 * 128].unflatten(1, (8, 128)))
+
+
+def test_no_tokens_and_no_sequences(kvq):
+    s = layer_state(kvq, 64, 32, [2, 1], 6)
+    q = s["qkv"][:, :s["nq"]]
+    none = kvq.kvq_paged_attend(q[:0], s["cache"], s["cu"] * 0, s["ln"], s["table"], max_q_len=1)
+    assert none.shape == (0, s["nq"], 64)
+    out = torch.full_like(q, 3.0)
+    kvq.kvq_paged_attend(q, s["cache"], s["cu"][:1], s["ln"][:0], s["table"][:0], max_q_len=1, out=out)
+    kvq.kvq_paged_attend(q, s["cache"], s["cu"] * 0, s["ln"], s["table"], max_q_len=1, out=out)
+    assert (out == 3.0).all()  # tokens of no sequence
+    kvq.kvq_paged_append(q[:0, :2], q[:0, :2], s["slots"][:0], s["cache"])
+    assert kvq.kvq_device_status() == 0
