@@ -361,10 +361,10 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       const uint32_t q = sbase + C::oQ + (item & 1) * C::QB;
       constexpr uint32_t id = instr_desc(kAccS32, kFmtS8, kFmtS8, false, false, 128, C::NQS);
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int b = 0; b < C::SBLK; ++b) {
         const int half = b / NG, j = b % NG;
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < C::G; x += 32) {
           const int byte = j * C::G + x;  // in the token's bytes
           const int abyte = C::TPR == 2 ? half * 64 + byte : byte;
@@ -381,9 +381,9 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       // one MMA for all groups of a 128-coordinate block
       constexpr uint32_t id = instr_desc(kAccS32, kFmtS8, kFmtU8, true, true, 128, C::NGM * C::NP);
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int mt = 0; mt < C::NCH; ++mt)
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < 4; ++x)
           mma_i8(tmem + 2 * C::SCOLS + (i % C::OBUF) * C::OCOLS + mt * C::NGM * C::NP,
                  smem_desc(v + mt * 16384 + x * 4096, 16, 1024, kSw128),
