@@ -223,7 +223,7 @@ kvq_status kvq_paged_attend(const void* q, kvq_dtype dtype, int64_t n_tokens, in
   a.dtype = dtype;
   a.rot = cache->rot;
   a.workspace = static_cast<uint8_t*>(workspace);
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 1 << 30;  // position - window stays in 32 bits
   a.qscale = sm_scale * kLog2e;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return from_cuda(cache->d == 64    ? kvq::launch_paged_attn<64>(a, max_q_len, dev.sm_count, st)

@@ -541,12 +541,19 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
       sh.vs[i & 3][t] = vtop * vmul;
       if (t == 0) sh.vexp[i & 3] = vexp;
       arrive(sh.scfull[i & 3]);
-      if (i >= KS) wait(sh.kfree[i % KS], i / KS - 1);
-      convert(kreg, ksc, ktop, sbase + C::oK + (i % KS) * C::TILE);
-      arrive(sh.kfull[i % KS]);
-      if (i >= KS) wait(sh.vfree[i % KS], i / KS - 1);
-      convert(vreg, vsc, vtop, sbase + C::oV + (i % KS) * C::TILE);
-      arrive(sh.vfull[i % KS]);
+      // K, then V through the same code (for the instruction cache)
+      float top = ktop;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        if (i >= KS) wait(kv ? sh.vfree[i % KS] : sh.kfree[i % KS], i / KS - 1);
+        convert(kreg, ksc, top, sbase + (kv ? C::oV : C::oK) + (i % KS) * C::TILE);
+        arrive(kv ? sh.vfull[i % KS] : sh.kfull[i % KS]);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) kreg[k] = vreg[k];
+#pragma unroll
+        for (int j = 0; j < NG; ++j) ksc[j] = vsc[j];
+        top = vtop;
+      }
       if (i + 1 < n) {
         wait(sh.dfull[(i + 1) % kPcRing], (i + 1) / kPcRing);
         load(i + 1);

@@ -432,6 +432,19 @@ def test_attend_chunk(kvq, dtype, rot, d, group, nq, heads, page, news, lens, wi
     run_attend(kvq, cache, q, cu, lens, table, window=window)
 
 
+@pytest.mark.parametrize("news", [[9, 1], [40, 200]])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 5000])
+def test_attend_wide_window(kvq, news, window):
+    """A window wider than everything is none, for tokens before position 0 too."""
+    lens = [7, 250]
+    cache = make_pool(kvq, 2, 20, 1, 16, 64, 64, 0)
+    table = make_batch(cache, 7, lens)
+    q = rows(gen(3), sum(news), 2, 64, torch.float16) * 0.25
+    a = run_attend(kvq, cache, q, [0, news[0], sum(news)], lens, table, window=window)
+    b = run_attend(kvq, cache, q, [0, news[0], sum(news)], lens, table)
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("d,group", [(64, 64), (128, 32), (256, 256)])
 @pytest.mark.parametrize("max_q", [1, 2, 16, 1000])
 def test_attend_any_hint(kvq, d, group, max_q):
