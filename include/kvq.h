@@ -395,7 +395,11 @@ KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtyp
  * h of that token and KV head h / n_q:
  *   s_t = sm_scale <q, K_t>,  out = sum_t softmax(s)_t V_t, rounded to dtype.
  * A token that attends no row gets zeros.  Rows of out that belong to no
- * sequence are left as they were.
+ * sequence are left as they were.  Products run on the tensor cores with fp32
+ * (or exact integer) sums.  Up to 16 query rows of a sequence and KV head
+ * (max_q_len * n_q): queries in 15-bit fixed point, weights in 23-bit.  More:
+ * rotated queries and weights rounded to fp16, and with g < d the ratios of a
+ * row's scales; a score is then off by at most 3 2^-12 sm_scale |q| |K_t|.
  *
  *   q          [n_tokens][n_kv_heads * n_q][d], token stride q_stride (read)
  *   out        same, token stride out_stride (written); must not overlap q

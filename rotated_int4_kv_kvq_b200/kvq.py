@@ -36,7 +36,6 @@ EXPORTS = ("kvq_rot_quant_fwd", "kvq_dequant_rot_inv", "kvq_rot_quant_fwd_lambda
            "kvq_paged_attend_workspace", "kvq_status_string", "kvq_device_status", "kvq_version")
 
 DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # kvq_dtype
-PAGE_SIZES = (16, 32, 64, 128, 256)
 
 
 class _PagedCacheC(ctypes.Structure):  # kvq_paged_cache
