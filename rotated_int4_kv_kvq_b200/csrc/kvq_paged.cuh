@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kvq_append_tile_kernel(cons
         if (pos < 0 || pos >= a.rope.n_pos) {
           flag_bad_index(status);
           slot = -1;
+          pos = 0;  // the lanes of a skipped row still read the table: its first row
         }
       }
     }
