@@ -359,209 +359,210 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
     if (lane == 0) mbar_arrive(smem_u32(&b));
   };
 
-  if (warp > C::W_PAGE) {
-    if constexpr (C::SPLIT) regs_dec<C::REGS_LESS>();  // idle
-  } else if (warp == C::W_PAGE) {
+  if (warp >= C::W_DEQ) {
+    // (here, before the warps part: all four of a warpgroup have to take the same
+    // one of these instructions.  The two warps behind the page warp are idle.)
     if constexpr (C::SPLIT) regs_dec<C::REGS_LESS>();
-    // ---------------- pages: what each tile is, and where ----------------
-    Cursor<M, KT> c;
-    c.seek(a, run.seq, run.off);
-    if (lane == 0) sh.begun = run.begin - c.tile;
-    for (int i = 0; i < n; ++i) {
-      PcTile& e = sh.tiles[i % kPcRing];
-      if (i >= kPcRing) wait(sh.dfree[i % kPcRing], i / kPcRing - 1);
-      const int t0 = (c.first + c.tile) * KT;
-      int64_t r = 0;
-      bool there = false;
-      if (lane < KT / 16) {
-        const int64_t t = int64_t(t0) + lane * 16;
-        if (t < c.q.len) {
-          const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
-          there = page >= 0 && page < a.n_pages;
-          if (there)
-            r = ((page * a.n_kv + c.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-          else
-            flag_bad_index(status);
+    if (warp == C::W_PAGE) {
+      // ---------------- pages: what each tile is, and where ----------------
+      Cursor<M, KT> c;
+      c.seek(a, run.seq, run.off);
+      if (lane == 0) sh.begun = run.begin - c.tile;
+      for (int i = 0; i < n; ++i) {
+        PcTile& e = sh.tiles[i % kPcRing];
+        if (i >= kPcRing) wait(sh.dfree[i % kPcRing], i / kPcRing - 1);
+        const int t0 = (c.first + c.tile) * KT;
+        int64_t r = 0;
+        bool there = false;
+        if (lane < KT / 16) {
+          const int64_t t = int64_t(t0) + lane * 16;
+          if (t < c.q.len) {
+            const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
+            there = page >= 0 && page < a.n_pages;
+            if (there)
+              r = ((page * a.n_kv + c.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+            else
+              flag_bad_index(status);
+          }
+          e.row[lane] = r;
         }
-        e.row[lane] = r;
+        const uint32_t have = __ballot_sync(kFull, there);
+        if (lane == 0) {
+          e.t0 = t0;
+          e.len = c.q.len;
+          e.c0 = c.q.c0;
+          e.head = c.head;
+          e.row0 = c.qt * M;
+          e.rows = int(min(int64_t(M), int64_t(c.q.n) * a.n_q - int64_t(c.qt) * M));
+          e.p0 = c.q.len - c.q.n;
+          e.starts = i == 0 || c.tile == 0;
+          e.last = c.tile + 1 == c.count;
+          e.ends = e.last || i + 1 == n;
+          e.have = have;
+        }
+        arrive(sh.dfull[i % kPcRing]);
+        if (i + 1 < n && ++c.tile == c.count) c.next_item(a);
       }
-      const uint32_t have = __ballot_sync(kFull, there);
-      if (lane == 0) {
-        e.t0 = t0;
-        e.len = c.q.len;
-        e.c0 = c.q.c0;
-        e.head = c.head;
-        e.row0 = c.qt * M;
-        e.rows = int(min(int64_t(M), int64_t(c.q.n) * a.n_q - int64_t(c.qt) * M));
-        e.p0 = c.q.len - c.q.n;
-        e.starts = i == 0 || c.tile == 0;
-        e.last = c.tile + 1 == c.count;
-        e.ends = e.last || i + 1 == n;
-        e.have = have;
-      }
-      arrive(sh.dfull[i % kPcRing]);
-      if (i + 1 < n && ++c.tile == c.count) c.next_item(a);
-    }
-  } else if (warp == C::W_MMA) {
-    if constexpr (C::SPLIT) regs_dec<C::REGS_LESS>();
-    // ---------------- MMA issue ----------------
-    constexpr uint32_t idS = instr_desc(kAccF32, kFmtF16, kFmtF16, false, false, 128, KT);
-    constexpr uint32_t idO = instr_desc(kAccF32, kFmtF16, kFmtF16, false, true, 128, D);
-    int items[2] = {0, 0}, used[2] = {0, 0};  // of each row tile: items and tiles it took part in
-    bool two = false;
-    auto scores = [&](int x, int i) {  // row tile x, tile i
-      const int slot = NT == 2 ? x : i & 1;
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t q = sbase + C::oQ + x * C::TILE, k = sbase + C::oK + (i % KS) * C::TILE;
+    } else if (warp == C::W_MMA) {
+      // ---------------- MMA issue ----------------
+      constexpr uint32_t idS = instr_desc(kAccF32, kFmtF16, kFmtF16, false, false, 128, KT);
+      constexpr uint32_t idO = instr_desc(kAccF32, kFmtF16, kFmtF16, false, true, 128, D);
+      int items[2] = {0, 0}, used[2] = {0, 0};  // of each row tile: items and tiles it took part in
+      bool two = false;
+      auto scores = [&](int x, int i) {  // row tile x, tile i
+        const int slot = NT == 2 ? x : i & 1;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t q = sbase + C::oQ + x * C::TILE, k = sbase + C::oK + (i % KS) * C::TILE;
 #pragma unroll 1
-        for (int s = 0; s < D / 16; ++s)
-          mma_f16(tmem + slot * 128, smem_desc(q + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128),
-                  smem_desc(k + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128), idS, s > 0);
-        mma_commit(bar(sh.sdone[slot]));
-        if (x == NT - 1 || !two) mma_commit(bar(sh.kfree[i % KS]));
-      }
-      __syncwarp();
-    };
-    auto values = [&](int x, int i, bool first) {
-      const int slot = NT == 2 ? x : i & 1;
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t v = sbase + C::oV + (i % KS) * C::TILE;
+          for (int s = 0; s < D / 16; ++s)
+            mma_f16(tmem + slot * 128,
+                    smem_desc(q + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128),
+                    smem_desc(k + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128), idS, s > 0);
+          mma_commit(bar(sh.sdone[slot]));
+          if (x == NT - 1 || !two) mma_commit(bar(sh.kfree[i % KS]));
+        }
+        __syncwarp();
+      };
+      auto values = [&](int x, int i, bool first) {
+        const int slot = NT == 2 ? x : i & 1;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t v = sbase + C::oV + (i % KS) * C::TILE;
 #pragma unroll 1
-        for (int s = 0; s < KT / 16; ++s)
-          mma_f16_ts(tmem + C::colO + x * 128, tmem + slot * 128 + s * 8,
-                     smem_desc(v + s * 2048, 16384, 1024, kSw128), idO, !first || s > 0);
-        mma_commit(bar(sh.odone[slot]));
-        if (x == NT - 1 || !two) mma_commit(bar(sh.vfree[i % KS]));
-      }
-      __syncwarp();
-    };
-    for (int i = 0; i < n; ++i) {
-      wait(sh.dfull[i % kPcRing], i / kPcRing);
-      const bool starts = sh.tiles[i % kPcRing].starts, ends = sh.tiles[i % kPcRing].ends;
-      const int rows = sh.tiles[i % kPcRing].rows;
-      // (this tile's scores are under way, so the softmax may be through with the
-      // description before it is read here)
-      arrive(sh.dfree[i % kPcRing]);
-      if (starts) {
-        two = NT == 2 && rows > 128;
-        wait(sh.qfull[0], items[0]++);
-        if (two) wait(sh.qfull[1], items[1]++);
-        wait(sh.kfull[i % KS], i / KS);
-        scores(0, i);
-        if (two) scores(1, i);
-      }
-      if constexpr (NT == 2) {
-        wait(sh.pfull[0], used[0]++);
-        wait(sh.vfull[i % KS], i / KS);
-        values(0, i, starts);
-        if (!ends) {
-          wait(sh.kfull[(i + 1) % KS], (i + 1) / KS);
-          scores(0, i + 1);
+          for (int s = 0; s < KT / 16; ++s)
+            mma_f16_ts(tmem + C::colO + x * 128, tmem + slot * 128 + s * 8,
+                       smem_desc(v + s * 2048, 16384, 1024, kSw128), idO, !first || s > 0);
+          mma_commit(bar(sh.odone[slot]));
+          if (x == NT - 1 || !two) mma_commit(bar(sh.vfree[i % KS]));
         }
-        if (two) {
-          wait(sh.pfull[1], used[1]++);
-          values(1, i, starts);
-          if (!ends) scores(1, i + 1);
+        __syncwarp();
+      };
+      for (int i = 0; i < n; ++i) {
+        wait(sh.dfull[i % kPcRing], i / kPcRing);
+        const bool starts = sh.tiles[i % kPcRing].starts, ends = sh.tiles[i % kPcRing].ends;
+        const int rows = sh.tiles[i % kPcRing].rows;
+        // (this tile's scores are under way, so the softmax may be through with the
+        // description before it is read here)
+        arrive(sh.dfree[i % kPcRing]);
+        if (starts) {
+          two = NT == 2 && rows > 128;
+          wait(sh.qfull[0], items[0]++);
+          if (two) wait(sh.qfull[1], items[1]++);
+          wait(sh.kfull[i % KS], i / KS);
+          scores(0, i);
+          if (two) scores(1, i);
         }
-      } else {
-        if (!ends) {
-          wait(sh.kfull[(i + 1) % KS], (i + 1) / KS);
-          scores(0, i + 1);
-        }
-        wait(sh.pfull[i & 1], i >> 1);
-        wait(sh.vfull[i % KS], i / KS);
-        values(0, i, starts);
-      }
-    }
-  } else if (warp >= C::W_DEQ) {
-    if constexpr (C::SPLIT) regs_dec<C::REGS_LESS>();
-    // ---------------- packed codes -> fp16 operands, a thread a token ----------------
-    const int t = tid - C::W_DEQ * 32;
-    constexpr int NP = D / 32;  // 16-byte pieces of a row
-    uint4 kreg[NP], vreg[NP];
-    float ksc[NG], vsc[NG];
-    auto load = [&](int i) {
-      const PcTile& e = sh.tiles[i % kPcRing];
-      const int64_t r = e.row[t >> 4] + (t & 15);
-      const uint4* kp = reinterpret_cast<const uint4*>(a.k_packed + r * (D / 2));
-      const uint4* vp = reinterpret_cast<const uint4*>(a.v_packed + r * (D / 2));
-      const bool there = (e.have >> (t >> 4) & 1u) && e.t0 + t < e.len;
-#pragma unroll
-      for (int k = 0; k < NP; ++k) kreg[k] = __ldg(kp + k), vreg[k] = __ldg(vp + k);
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {  // rows past the end may hold anything
-        ksc[j] = there ? __ldg(a.k_scales + r * NG + j) : 0.0f;
-        vsc[j] = there ? __ldg(a.v_scales + r * NG + j) : 0.0f;
-      }
-    };
-    auto convert = [&](const uint4 (&w)[NP], const float (&sc)[NG], float top, uint32_t tile) {
-      const float inv = top > 0.0f ? 1.0f / top : 0.0f;
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        uint32_t f = 0;
-        if constexpr (NG > 1) {
-          const float x = sc[k * 32 / C::G] * inv;
-          f = float2_to_half2_bits(x, x);
-        }
-        const uint32_t words[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 h = codes_to_half(words[j]);
-          if constexpr (NG > 1)
-            h = make_uint4(hmul2(h.x, f), hmul2(h.y, f), hmul2(h.z, f), hmul2(h.w, f));
-          const int c = (k & 1) * 4 + j;  // 16-byte column of the 128
-          sts128(tile + uint32_t(k / 2) * 16384 + uint32_t(t) * 128 +
-                     (uint32_t(c ^ (t & 7)) << 4),
-                 h.x, h.y, h.z, h.w);
+        if constexpr (NT == 2) {
+          wait(sh.pfull[0], used[0]++);
+          wait(sh.vfull[i % KS], i / KS);
+          values(0, i, starts);
+          if (!ends) {
+            wait(sh.kfull[(i + 1) % KS], (i + 1) / KS);
+            scores(0, i + 1);
+          }
+          if (two) {
+            wait(sh.pfull[1], used[1]++);
+            values(1, i, starts);
+            if (!ends) scores(1, i + 1);
+          }
+        } else {
+          if (!ends) {
+            wait(sh.kfull[(i + 1) % KS], (i + 1) / KS);
+            scores(0, i + 1);
+          }
+          wait(sh.pfull[i & 1], i >> 1);
+          wait(sh.vfull[i % KS], i / KS);
+          values(0, i, starts);
         }
       }
-      fence_proxy_async_smem();
-    };
-    auto largest = [](const float (&s)[NG]) {
-      float x = s[0];
+    } else if (warp < C::W_MMA) {
+      // ---------------- packed codes -> fp16 operands, a thread a token ----------------
+      const int t = tid - C::W_DEQ * 32;
+      constexpr int NP = D / 32;  // 16-byte pieces of a row
+      uint4 kreg[NP], vreg[NP];
+      float ksc[NG], vsc[NG];
+      auto load = [&](int i) {
+        const PcTile& e = sh.tiles[i % kPcRing];
+        const int64_t r = e.row[t >> 4] + (t & 15);
+        const uint4* kp = reinterpret_cast<const uint4*>(a.k_packed + r * (D / 2));
+        const uint4* vp = reinterpret_cast<const uint4*>(a.v_packed + r * (D / 2));
+        const bool there = (e.have >> (t >> 4) & 1u) && e.t0 + t < e.len;
 #pragma unroll
-      for (int j = 1; j < NG; ++j) x = fmaxf(x, s[j]);
-      return x;
-    };
-    int vexp = -126;
-    wait(sh.dfull[0], 0);
-    load(0);
-    for (int i = 0; i < n; ++i) {
-      if (sh.tiles[i % kPcRing].starts) vexp = -126;
-      const float ktop = largest(ksc), vtop = largest(vsc);
-      // the V scales of the tile under a power of two that only grows
-      float x = vtop;
+        for (int k = 0; k < NP; ++k) kreg[k] = __ldg(kp + k), vreg[k] = __ldg(vp + k);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-      if (lane == 0) sh.wmax[i & 1][warp - C::W_DEQ] = x;
-      named_sync(3, 128);
+        for (int j = 0; j < NG; ++j) {  // rows past the end may hold anything
+          ksc[j] = there ? __ldg(a.k_scales + r * NG + j) : 0.0f;
+          vsc[j] = there ? __ldg(a.v_scales + r * NG + j) : 0.0f;
+        }
+      };
+      auto convert = [&](const uint4 (&w)[NP], const float (&sc)[NG], float top, uint32_t tile) {
+        const float inv = top > 0.0f ? 1.0f / top : 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.wmax[i & 1][w]);
-      vexp = max(vexp, min(int(__float_as_uint(x) >> 23) - 126, 126));
-      const float vmul = __uint_as_float(uint32_t(127 - vexp) << 23);
-      // ring of four: the softmax of tile i - 4 is behind V's wait of tile i - 1
-      sh.ks[i & 3][t] = ktop;
-      sh.vs[i & 3][t] = vtop * vmul;
-      if (t == 0) sh.vexp[i & 3] = vexp;
-      arrive(sh.scfull[i & 3]);
-      // K, then V through the same code (for the instruction cache)
-      float top = ktop;
+        for (int k = 0; k < NP; ++k) {
+          uint32_t f = 0;
+          if constexpr (NG > 1) {
+            const float x = sc[k * 32 / C::G] * inv;
+            f = float2_to_half2_bits(x, x);
+          }
+          const uint32_t words[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 h = codes_to_half(words[j]);
+            if constexpr (NG > 1)
+              h = make_uint4(hmul2(h.x, f), hmul2(h.y, f), hmul2(h.z, f), hmul2(h.w, f));
+            const int c = (k & 1) * 4 + j;  // 16-byte column of the 128
+            sts128(tile + uint32_t(k / 2) * 16384 + uint32_t(t) * 128 +
+                       (uint32_t(c ^ (t & 7)) << 4),
+                   h.x, h.y, h.z, h.w);
+          }
+        }
+        fence_proxy_async_smem();
+      };
+      auto largest = [](const float (&s)[NG]) {
+        float x = s[0];
+#pragma unroll
+        for (int j = 1; j < NG; ++j) x = fmaxf(x, s[j]);
+        return x;
+      };
+      int vexp = -126;
+      wait(sh.dfull[0], 0);
+      load(0);
+      for (int i = 0; i < n; ++i) {
+        if (sh.tiles[i % kPcRing].starts) vexp = -126;
+        const float ktop = largest(ksc), vtop = largest(vsc);
+        // the V scales of the tile under a power of two that only grows
+        float x = vtop;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+        if (lane == 0) sh.wmax[i & 1][warp - C::W_DEQ] = x;
+        named_sync(3, 128);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.wmax[i & 1][w]);
+        vexp = max(vexp, min(int(__float_as_uint(x) >> 23) - 126, 126));
+        const float vmul = __uint_as_float(uint32_t(127 - vexp) << 23);
+        // ring of four: the softmax of tile i - 4 is behind V's wait of tile i - 1
+        sh.ks[i & 3][t] = ktop;
+        sh.vs[i & 3][t] = vtop * vmul;
+        if (t == 0) sh.vexp[i & 3] = vexp;
+        arrive(sh.scfull[i & 3]);
+        // K, then V through the same code (for the instruction cache)
+        float top = ktop;
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        if (i >= KS) wait(kv ? sh.vfree[i % KS] : sh.kfree[i % KS], i / KS - 1);
-        convert(kreg, ksc, top, sbase + (kv ? C::oV : C::oK) + (i % KS) * C::TILE);
-        arrive(kv ? sh.vfull[i % KS] : sh.kfull[i % KS]);
+        for (int kv = 0; kv < 2; ++kv) {
+          if (i >= KS) wait(kv ? sh.vfree[i % KS] : sh.kfree[i % KS], i / KS - 1);
+          convert(kreg, ksc, top, sbase + (kv ? C::oV : C::oK) + (i % KS) * C::TILE);
+          arrive(kv ? sh.vfull[i % KS] : sh.kfull[i % KS]);
 #pragma unroll
-        for (int k = 0; k < NP; ++k) kreg[k] = vreg[k];
+          for (int k = 0; k < NP; ++k) kreg[k] = vreg[k];
 #pragma unroll
-        for (int j = 0; j < NG; ++j) ksc[j] = vsc[j];
-        top = vtop;
-      }
-      if (i + 1 < n) {
-        wait(sh.dfull[(i + 1) % kPcRing], (i + 1) / kPcRing);
-        load(i + 1);
+          for (int j = 0; j < NG; ++j) ksc[j] = vsc[j];
+          top = vtop;
+        }
+        if (i + 1 < n) {
+          wait(sh.dfull[(i + 1) % kPcRing], (i + 1) / kPcRing);
+          load(i + 1);
+        }
       }
     }
   } else {
