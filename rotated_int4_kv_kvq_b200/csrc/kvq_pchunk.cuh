@@ -453,22 +453,31 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
           scores(0, i);
           if (two) scores(1, i);
         }
+        // The next scores overwrite columns whose P the values before them read: only
+        // products of one accumulator are ordered among themselves, so these wait.
         if constexpr (NT == 2) {
-          wait(sh.pfull[0], used[0]++);
+          wait(sh.pfull[0], used[0]);
           wait(sh.vfull[i % KS], i / KS);
           values(0, i, starts);
           if (!ends) {
             wait(sh.kfull[(i + 1) % KS], (i + 1) / KS);
+            wait(sh.odone[0], used[0]);
             scores(0, i + 1);
           }
+          ++used[0];
           if (two) {
-            wait(sh.pfull[1], used[1]++);
+            wait(sh.pfull[1], used[1]);
             values(1, i, starts);
-            if (!ends) scores(1, i + 1);
+            if (!ends) {
+              wait(sh.odone[1], used[1]);
+              scores(1, i + 1);
+            }
+            ++used[1];
           }
         } else {
           if (!ends) {
             wait(sh.kfull[(i + 1) % KS], (i + 1) / KS);
+            if (i > 0) wait(sh.odone[(i + 1) & 1], (i - 1) >> 1);
             scores(0, i + 1);
           }
           wait(sh.pfull[i & 1], i >> 1);
