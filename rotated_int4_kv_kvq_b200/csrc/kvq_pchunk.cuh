@@ -13,9 +13,13 @@
 //   p = 2^(S s_K[t] c_row - m)      f32; the row's reference m moves only when
 //                    its maximum exceeds it by 8, so the accumulators are
 //                    rescaled rarely
-//   O += P C_V       P = p s_V[t] 2^-v in fp16 (error 2^-12 of a weight, as in
-//                    any fp16 product), v a power of two that the V scales
-//                    seen so far stay under
+//   O += P C_V       P = p s_V[t] 2^-v in fp16 (error 2^-11 of a weight, as in
+//                    any fp16 product, or 2^-31 of the largest scale where that is
+//                    more), v the row's own: the V scales that it has attended so
+//                    far stay under 2^(v + 7).  Cached rows that it does not attend
+//                    have no say in v: tiles with a mask look for the largest scale
+//                    seen.  Scales lie in shared memory over their tile's power of
+//                    two; the difference of the exponents joins the reference m.
 // With several scales a row (g < d) a row's largest scale is kept apart in f32
 // and the codes are multiplied by the ratios s_j / s_max, rounded to fp16.
 //
@@ -79,7 +83,7 @@ struct PcShared {
   PcTile tiles[kPcRing];
   uint32_t tmem;
   int64_t begun;
-  float ks[4][128], vs[4][128];  // by tile: K scales; V scales over 2^vexp
+  float ks[4][128], vs[4][128];  // by tile: K scales; V scales over 2^vexp, below 2^7
   int vexp[4];
   float wmax[2][4];
   uint32_t sign_in[128], sign_out[128];  // sign masks of a row's words (of each thread of a pair)
@@ -534,13 +538,11 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         for (int j = 1; j < NG; ++j) x = fmaxf(x, s[j]);
         return x;
       };
-      int vexp = -126;
       wait(sh.dfull[0], 0);
       load(0);
       for (int i = 0; i < n; ++i) {
-        if (sh.tiles[i % kPcRing].starts) vexp = -126;
         const float ktop = largest(ksc), vtop = largest(vsc);
-        // the V scales of the tile under a power of two that only grows
+        // the V scales of the tile under a power of two
         float x = vtop;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         named_sync(3, 128);
 #pragma unroll
         for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.wmax[i & 1][w]);
-        vexp = max(vexp, min(int(__float_as_uint(x) >> 23) - 126, 126));
+        const int vexp = max(int(__float_as_uint(x) >> 23) - 133, -126);
         const float vmul = __uint_as_float(uint32_t(127 - vexp) << 23);
         // ring of four: the softmax of tile i - 4 is behind V's wait of tile i - 1
         sh.ks[i & 3][t] = ktop;
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
     const uint32_t qtile = sbase + C::oQ + x * C::TILE;
     const uint32_t stage = qtile + w4 * 4096;  // this warp's rows of it, 4 KB of every 16
     float m = 0.0f, l = 0.0f, rowc = 0.0f;
-    int used = 0, item = -1, vexp = 0, pos = 0;
+    int used = 0, item = -1, vexp = 0, pos = 0;  // vexp: v of the row
     bool active = false;
     for (int i = 0; i < n; ++i) {
       wait(sh.dfull[i % kPcRing], i / kPcRing);
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
           // (All loops over columns are rolled: what the roles run per tile has to
           // stay in the instruction cache.  Unrolled, one pass took 1.6 times as
           // long.)
-          float top = -INFINITY, top1 = -INFINITY;
+          float top = -INFINITY, top1 = -INFINITY, vtop = 0.0f;
           auto largest = [&](auto masks) {
             constexpr bool MASK = decltype(masks)::value;
 #pragma unroll 1
@@ -673,6 +675,10 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
                   u = mk2(sm >> j & 1u ? lo2(u) : -INFINITY, sm >> (j + 1) & 1u ? hi2(u) : -INFINITY);
                   w = mk2(sm >> (j + 2) & 1u ? lo2(w) : -INFINITY,
                           sm >> (j + 3) & 1u ? hi2(w) : -INFINITY);
+                  const float4 v = vs4[(c + j) / 4];
+                  vtop = max3f(vtop, sm >> j & 1u ? v.x : 0.0f, sm >> (j + 1) & 1u ? v.y : 0.0f);
+                  vtop = max3f(vtop, sm >> (j + 2) & 1u ? v.z : 0.0f,
+                               sm >> (j + 3) & 1u ? v.w : 0.0f);
                 }
                 top = max3f(top, lo2(u), hi2(u));
                 top1 = max3f(top1, lo2(w), hi2(w));
@@ -686,13 +692,17 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
           top = fmaxf(top, top1) * rowc;  // (0 for rows that are not there)
           if (!(top > -INFINITY)) top = -3e38f;
           const bool moved = top > m + 8.0f;
-          if (__any_sync(kFull, moved) || ve != vexp) {
+          int vn = max(vexp, ve);
+          if (!whole)  // (a tile's scales reach down to 2^-100 of its largest)
+            vn = vtop > 0.0f ? max(vexp, ve + max(int(__float_as_uint(vtop) >> 23) - 133, -100))
+                             : vexp;
+          if (__any_sync(kFull, moved || vn != vexp)) {
             const float mn = moved ? top : m;
             const float f = ex2(m - mn);
-            const float fo = f * ex2(float(max(vexp - ve, -200)));
+            const float fo = f * ex2(float(max(vexp - vn, -200)));
             l *= f;
             m = mn;
-            vexp = ve;
+            vexp = vn;
             if (!e.starts) {
               wait(sh.odone[NT == 2 ? x : (i - 1) & 1], NT == 2 ? used - 1 : (i - 1) >> 1);
               tc_fence_after();
@@ -712,7 +722,12 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         // ---- weights ----
         auto weights = [&](auto masks) {
           constexpr bool MASK = decltype(masks)::value;
-          const f2 rc2 = mk2(rowc, rowc), nm2 = mk2(-m, -m);
+          // P = p 2^dv times the scale as it lies there; l takes the 2^dv out again.
+          // (From 2^-40 on P is below fp16's smallest: no matter how far.  Upwards the
+          // limit is out of reach but for rows that attend none of the tile.)
+          const int dv = min(max(ve - vexp, -40), 100);
+          const float nm = float(dv) - m;
+          const f2 rc2 = mk2(rowc, rowc), nm2 = mk2(nm, nm);
           f2 l2 = mk2(0.0f, 0.0f);
 #pragma unroll 1
           for (int c = 0; c < KT; c += 32) {
@@ -742,7 +757,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
             }
             tmem_st16(tS + c / 2, p);  // over columns of S that have been read
           }
-          l += lo2(l2) + hi2(l2);
+          l = fmaf(lo2(l2) + hi2(l2), __uint_as_float(uint32_t(127 - dv) << 23), l);
         };
         if (whole)
           weights(std::false_type{});

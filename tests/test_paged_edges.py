@@ -2,13 +2,18 @@
 tables, rows that a mask hides, weights far below the largest, queries that are
 not finite, padding.  Helpers and tolerances: test_paged.py."""
 
+import numpy as np
 import pytest
 import torch
 
+import oracle.kvq_oracle as O
 from rotated_int4_kv_kvq_b200 import workloads as W
-from test_paged import gen, kvq, rows  # noqa: F401
+from test_paged import (BOTH, attend_tolerance, gen, kvq, make_batch, make_pool, np64,
+                         rows)  # noqa: F401
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:invalid value:RuntimeWarning")]
+
+SHAPES = [(64, 64), (64, 32), (128, 128), (128, 32), (256, 256), (256, 64)]
 
 
 @pytest.mark.parametrize("inter", [False, True])
@@ -43,3 +48,38 @@ def test_append_many_rows_far_positions(kvq, d, group, inter):
     for b in out[1][:4]:
         assert (b[bad] == 0).all()
     assert (out[1][4][bad] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("window", [0, 30])
+def test_attend_hidden_values_of_any_size(kvq, dtype, d, group, window):
+    """Values 2^30 (fp16: 2^18) times as large in rows that a token does not attend (later ones;
+    with a window earlier ones too) leave its result as exact as any other."""
+    n = 330
+    cache = make_pool(kvq, d, 24, 2, 16, d, group, 0)
+    table = make_batch(cache, 6, [n])
+    at = torch.arange(n, device="cuda")
+    page, off = table[0].long()[at // 16], at % 16
+    a, b = (150, 260) if window else (100, n)
+    cache.v_scales[page[a:b], :, off[a:b]] *= 2.0 ** (18 if dtype == torch.float16 else 30)
+    cache.v_scales *= 2.0 ** -8  # what an fp16 result can hold
+    q = rows(gen(3), n, 4, d, dtype) * 0.25
+    dev = dict(device="cuda", dtype=torch.int32)
+    got = kvq.kvq_paged_attend(q, cache, torch.tensor([0, n], **dev), torch.tensor([n], **dev),
+                               table, max_q_len=n, window=window)
+    assert kvq.kvq_device_status() == 0
+    pools, tab = [x.cpu().numpy() for x in cache.tensors()[:4]], table.cpu().numpy()
+    ref = O.attend_paged(np64(q), *pools, [0, n], [n], tab, cache.signs.cpu().numpy(), 0, group,
+                         d ** -0.5, window)
+    tol = attend_tolerance(np64(q), ref, pools, [0, n], [n], tab, cache, d ** -0.5, window, dtype)
+    # A token that does attend some of them: besides 2^-11 of itself a weight times its
+    # scale is off by half of fp16's smallest step, 2^-25, in units of 2^v, and 2^(v + 6)
+    # is at most the largest attended scale S.  Each of up to n rows: 2^-31 S times a
+    # code vector of at most 7 sqrt(d), over a sum of weights of at least 1.
+    i = np.arange(n)
+    none = (i < a) | (i - window >= b - 1) if window else i < a
+    tol[~none] += n * 2.0 ** -31 * float(cache.v_scales.max()) * 7 * d ** 0.5
+    assert none.sum() >= 100
+    err = np.abs(np64(got) - ref)
+    assert np.all(err <= tol), f"{(err / tol).max():.3g} x tolerance"
