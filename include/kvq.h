@@ -406,9 +406,11 @@ KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtyp
  *   cu_q       [n_seqs + 1] int32, non-decreasing, 0 .. n_tokens
  *   kv_len     [n_seqs] int32, 0 .. max_pages * page_size
  *   page_table [n_seqs][max_pages] int32; entries past a sequence's last
- *              page are not read.  Rows of a page outside the pool are not
- *              attended, and a sequence whose cu_q or kv_len is out of range
- *              is treated as having no tokens (KVQ_ERR_BAD_INDEX).
+ *              page, and those of pages wholly before the window of its first
+ *              token, are not read (such pages may be released: -1).  Rows of
+ *              a page outside the pool are not attended, and a sequence whose
+ *              cu_q or kv_len is out of range is treated as having no tokens
+ *              (KVQ_ERR_BAD_INDEX).
  *   n_q        1..64 queries per KV head; n_kv_heads * n_q <= 65535
  *   max_q_len  the largest number of new tokens of a sequence: a hint that
  *              chooses the kernel; the result is right for any value >= 1

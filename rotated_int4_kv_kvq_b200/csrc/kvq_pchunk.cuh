@@ -66,7 +66,7 @@ struct Pc {
 };
 
 struct PcTile {
-  int t0, len, c0, head, row0, rows, p0;
+  int t0, lo, hi, c0, head, row0, rows, p0;  // (the item attends tokens lo .. hi - 1)
   int starts, last, ends;
   uint32_t have;
   int64_t row[8];
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         bool there = false;
         if (lane < KT / 16) {
           const int64_t t = int64_t(t0) + lane * 16;
-          if (t < c.q.len) {
+          if (t < c.hi && t + 15 >= c.lo) {
             const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
             there = page >= 0 && page < a.n_pages;
             if (there)
@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         const uint32_t have = __ballot_sync(kFull, there);
         if (lane == 0) {
           e.t0 = t0;
-          e.len = c.q.len;
+          e.lo = c.lo;
+          e.hi = c.hi;
           e.c0 = c.q.c0;
           e.head = c.head;
           e.row0 = c.qt * M;
@@ -500,11 +501,12 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         const int64_t r = e.row[t >> 4] + (t & 15);
         const uint4* kp = reinterpret_cast<const uint4*>(a.k_packed + r * (D / 2));
         const uint4* vp = reinterpret_cast<const uint4*>(a.v_packed + r * (D / 2));
-        const bool there = (e.have >> (t >> 4) & 1u) && e.t0 + t < e.len;
+        const bool there =
+            (e.have >> (t >> 4) & 1u) && e.t0 + t >= e.lo && e.t0 + t < e.hi;
 #pragma unroll
         for (int k = 0; k < NP; ++k) kreg[k] = __ldg(kp + k), vreg[k] = __ldg(vp + k);
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {  // rows past the end may hold anything
+        for (int j = 0; j < NG; ++j) {  // rows that no query attends may hold anything
           ksc[j] = there ? __ldg(a.k_scales + r * NG + j) : 0.0f;
           vsc[j] = there ? __ldg(a.v_scales + r * NG + j) : 0.0f;
         }
@@ -640,7 +642,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         const int pf = __shfl_sync(kFull, pos, 0), pl = __shfl_sync(kFull, pos, 31);
         const bool whole = e.t0 + KT - 1 <= pf && (a.window == 0 || e.t0 > pl - a.window) &&
                            e.have == 0xFFu;
-        const int hi = min(pos, e.len - 1) - e.t0;                     // last column seen
+        const int hi = pos - e.t0;                                     // last column seen
         const int lo = a.window > 0 ? pos - a.window + 1 - e.t0 : 0;   // first
         auto seen = [&](int c) {  // bit j: column c + j of 32 is seen
           const int l = max(lo - c, 0), h = min(hi - c, 31);

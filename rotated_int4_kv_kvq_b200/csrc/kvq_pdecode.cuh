@@ -104,11 +104,11 @@ struct Pd {
 
 // A tile as the page warp writes it down for the others, up to a ring ahead.
 struct PdTile {
-  int t0, len;          // first token, cached rows of the sequence
+  int t0, lo, hi;       // first token; the item attends tokens lo .. hi - 1
   int c0, head, row0, rows;
   int starts, ends;     // first, last tile of its item (or of the block's share)
   int whole, last;      // no row's limits lie inside; the item's last tile
-  uint32_t have;        // bit i: tokens 16 i .. 16 i + 15 are there
+  uint32_t have;        // bit i: some of tokens 16 i .. 16 i + 15 are attended, and there
   int64_t row[16];      // cache row of each 16 tokens (0 where they are not)
 };
 constexpr int kPdRing = 8;
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       bool there = false;
       if (lane < KT / 16) {
         const int64_t t = int64_t(t0) + lane * 16;
-        if (t < c.q.len) {
+        if (t < c.hi && t + 15 >= c.lo) {
           const int64_t page = __ldg(a.page_table + c.seq * a.max_pages + (t >> a.page_shift));
           there = page >= 0 && page < a.n_pages;
           if (there)
@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
         const int pl = c.q.len - c.q.n + (row0 + rows - 1) / a.n_q;
         e.have = have;
         e.t0 = t0;
-        e.len = c.q.len;
+        e.lo = c.lo;
+        e.hi = c.hi;
         e.c0 = c.q.c0;
         e.head = c.head;
         e.row0 = row0;
@@ -520,9 +521,9 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       for (int h = 0; h < TPR; ++h) {
         const int tl = row + 128 * h;
         const float* sc = reinterpret_cast<const float*>(smem + C::oS + (i & 1) * 2 * C::SC) + tl * NG;
-        seen[h] = e.whole || (e.t0 + tl < e.len && (e.have >> (tl >> 4) & 1u));
+        seen[h] = e.whole || (e.t0 + tl >= e.lo && e.t0 + tl < e.hi && (e.have >> (tl >> 4) & 1u));
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {  // rows past the end may hold anything
+        for (int j = 0; j < NG; ++j) {  // rows that no query attends may hold anything
           ks[h][j] = seen[h] ? sc[j] : 0.0f;
           vs[h][j] = seen[h] ? sc[C::SC / 4 + j] : 0.0f;
         }

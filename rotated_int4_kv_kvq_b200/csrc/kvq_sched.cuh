@@ -27,23 +27,29 @@ __device__ __forceinline__ SeqInfo load_seq(const PagedAttnArgs& a, int s, unsig
   return SeqInfo{b, e - b, len};
 }
 
-// Tiles of cached rows of row tile qt: first tile and their number.  (32-bit
-// arithmetic: rows, positions and lengths are below 2^31.)
+// Row tile qt: the cached rows that some query of it attends, lo .. hi - 1 (none if
+// hi <= lo), and their tiles, the first and their number.  What the other rows hold,
+// and whether their pages are there, must not matter.  (32-bit arithmetic: rows,
+// positions and lengths are below 2^31.)
+struct ItemTiles {
+  int lo, hi, first, count;
+};
 template <int M, int KT>
-__device__ __forceinline__ void item_tiles(const PagedAttnArgs& a, const SeqInfo& q, int qt,
-                                           int& first, int& count) {
+__device__ __forceinline__ ItemTiles item_tiles(const PagedAttnArgs& a, const SeqInfo& q, int qt) {
   const unsigned row = unsigned(qt) * M, rows = unsigned(q.n) * unsigned(a.n_q);
   const unsigned last = min(rows, row + M) - 1;
   const int p0 = q.len - q.n + int(row / unsigned(a.n_q));
-  const int hi = q.len - q.n + int(last / unsigned(a.n_q)) + 1;
-  const int lo = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
-  if (hi <= lo) {
-    first = 0;
-    count = 1;
+  ItemTiles t;
+  t.hi = q.len - q.n + int(last / unsigned(a.n_q)) + 1;
+  t.lo = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
+  if (t.hi <= t.lo) {
+    t.first = 0;
+    t.count = 1;
   } else {
-    first = int(unsigned(lo) / KT);
-    count = int((unsigned(hi) + KT - 1) / KT) - first;
+    t.first = int(unsigned(t.lo) / KT);
+    t.count = int((unsigned(t.hi) + KT - 1) / KT) - t.first;
   }
+  return t;
 }
 
 template <int M>
@@ -68,9 +74,7 @@ __device__ __forceinline__ int64_t head_units(const PagedAttnArgs& a, const SeqI
   const int nqt = row_tiles<M>(a, q);
 #pragma unroll 1
   for (int qt = WARP ? threadIdx.x & 31 : 0; qt < nqt; qt += WARP ? 32 : 1) {
-    int f, c;
-    item_tiles<M, KT>(a, q, qt, f, c);
-    u += c;
+    u += item_tiles<M, KT>(a, q, qt).count;
   }
   return WARP ? __shfl_sync(kFull, warp_scan(u), 31) : u;
 }
@@ -79,10 +83,11 @@ __device__ __forceinline__ int64_t head_units(const PagedAttnArgs& a, const SeqI
 template <int M, int KT>
 struct Cursor {
   SeqInfo q;
-  int seq, head, qt, nqt, first, count, tile;
+  int seq, head, qt, nqt, lo, hi, first, count, tile;
 
   __device__ __forceinline__ void item(const PagedAttnArgs& a) {
-    item_tiles<M, KT>(a, q, qt, first, count);
+    const ItemTiles t = item_tiles<M, KT>(a, q, qt);
+    lo = t.lo, hi = t.hi, first = t.first, count = t.count;
   }
   // To the first unit of the next item; the caller knows that there is one.
   __device__ __forceinline__ void next_item(const PagedAttnArgs& a) {
@@ -116,8 +121,7 @@ struct Cursor {
     off -= head * per_head;
     const int lane = threadIdx.x & 31;
     for (int base = 0;; base += 32) {  // the lanes count 32 row tiles at a time
-      int f = 0, c = 0;
-      if (base + lane < nqt) item_tiles<M, KT>(a, q, base + lane, f, c);
+      const int c = base + lane < nqt ? item_tiles<M, KT>(a, q, base + lane).count : 0;
       const int64_t end = warp_scan(c);
       const uint32_t past = __ballot_sync(kFull, end > off);
       if (past != 0) {

@@ -9,7 +9,7 @@ import torch
 import oracle.kvq_oracle as O
 from rotated_int4_kv_kvq_b200 import workloads as W
 from test_paged import (BOTH, attend_tolerance, gen, kvq, make_batch, make_pool, np64,
-                         rows)  # noqa: F401
+                         poison, rows, run_attend)  # noqa: F401
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:invalid value:RuntimeWarning")]
 
@@ -83,3 +83,28 @@ def test_attend_hidden_values_of_any_size(kvq, dtype, d, group, window):
     assert none.sum() >= 100
     err = np.abs(np64(got) - ref)
     assert np.all(err <= tol), f"{(err / tol).max():.3g} x tolerance"
+
+
+@pytest.mark.parametrize("kind", ["released", "unwritten"])
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("nq,page,news,lens,window", [
+    (4, 16, [1, 1], [1000, 333], 40), (2, 32, [4, 3], [700, 2000], 129), (1, 16, [1], [470], 1),
+    (4, 16, [70, 33], [600, 433], 50), (3, 64, [300], [1500], 256), (16, 16, [9], [340], 17)])
+def test_attend_pages_before_the_window(kvq, kind, d, group, nq, page, news, lens, window):
+    """Pages that lie wholly before every token's window are not looked at: they may
+    be released (-1), or hold whatever fresh memory does."""
+    cache = make_pool(kvq, d + nq, sum(-(-m // page) for m in lens) + 2, 2, page, d, group, 0)
+    table = make_batch(cache, 6, lens)
+    poison(cache, table, lens)
+    for s, (n, m) in enumerate(zip(news, lens)):
+        free = max(0, m - n - window + 1) // page
+        assert free > 0
+        if kind == "released":
+            table[s, :free] = -1
+        else:
+            gone = table[s, :free].long()
+            cache.k_scales[gone], cache.v_scales[gone] = float("nan"), float("inf")
+            cache.v_scales[gone[0]] = float("nan")
+    cu = np.concatenate([[0], np.cumsum(news)]).tolist()
+    q = rows(gen(nq), cu[-1], 2 * nq, d, torch.float16) * 0.25
+    run_attend(kvq, cache, q, cu, lens, table, window=window)
