@@ -397,7 +397,8 @@ KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtyp
  * A token that attends no row gets zeros.  Rows of out that belong to no
  * sequence are left as they were.  Products run on the tensor cores with fp32
  * (or exact integer) sums.  Up to 16 query rows of a sequence and KV head
- * (max_q_len * n_q): queries in 15-bit fixed point, weights in 23-bit.  More:
+ * (max_q_len * n_q): queries in 15-bit fixed point (2^-15 of the largest rotated
+ * value), weights times V scales in 32-bit (2^-28 of the largest).  More:
  * rotated queries and weights rounded to fp16, and with g < d the ratios of a
  * row's scales; a score is then off by at most 3 2^-12 sm_scale |q| |K_t|.
  *

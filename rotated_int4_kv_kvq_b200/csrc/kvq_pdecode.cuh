@@ -16,16 +16,21 @@
 //            Q: each rotated query in 15-bit fixed point, two 7-bit slices
 //            (error 2^-15 of its largest coordinate)
 //   values   O[i][n] = sum_t 16 c_V[t][i] P[t][n]     kind::i8, s32
-//            P: weight times V scale in 23-bit fixed point, three 8-bit
-//            slices (error 2^-17 of the largest so far)
+//            P: weight times V scale in 32-bit fixed point, four 8-bit
+//            slices (error 2^-28 of the largest so far)
 // With several scales a row (g < d) the scores of each group accumulate in
 // columns of their own and each group of coordinates takes the P that carries
 // its scale; O keeps only those blocks.
 //
 // Online softmax: the reference of a query moves only when a score exceeds it
 // by 7 in log2, the fixed point of P when a weight would overflow; either is
-// found by the vote in the barrier that P needs anyway.  O is read back and
-// accumulated in fp32 after every tile, so it is never rescaled in place.
+// found by the vote in the barrier that P needs anyway.  Weights below half a step
+// of P are lost, of a tail of n faint tokens at most n 2^-28 of the largest; hence
+// four slices (three, with 7 bits of room: n 2^-17), and what P is made for only 4
+// bits below its top.  (The two batches below take 269 / 197 us with 2 bits of room
+// and 263 / 185 with 8, as tiles' maxima differ; with a vote that follows the tail
+// down instead 317 / 210.)  O is read back and accumulated in fp32 after every tile,
+// so it is never rescaled in place.
 //
 // A tile is 128 smem rows of 128 bytes (two tokens a row at d = 64, half a
 // token at d = 256).  A block is a pipeline of roles: four warps expand codes
@@ -73,7 +78,7 @@ struct Pd {
   static constexpr int KT = 128 * TPR;            // tokens of a tile
   static constexpr int NQS = max_of(16, 2 * R);   // N of the score MMA
   static constexpr int SBLK = TPR * NG;           // its column blocks
-  // bytes of P of a token and group (3 R, to a swizzle width)
+  // bytes of P of a token and group (4 R, to a swizzle width)
   static constexpr int PW = R <= 4 && TPR == 2 ? 16 : (R <= 8 ? 32 : 64);
   static constexpr int NP = TPR * PW;             // N of the value MMA, for a group
   static constexpr int NGM = D == 256 ? max_of(1, NG / 2) : NG;  // P's of a 128-coordinate block
@@ -213,13 +218,15 @@ __device__ __forceinline__ float* part_slot(const PagedAttnArgs& a, int block, i
   return a.parts + (int64_t(block) * 2 + slot) * part_floats<D, R>();
 }
 
-// Four 23-bit weights -> slice words (byte k of every weight).
+// Four weights -> slice words (byte k of every weight).
 __device__ __forceinline__ void pd_slices(const uint32_t* w, uint32_t& b0, uint32_t& b1,
-                                          uint32_t& b2) {
+                                          uint32_t& b2, uint32_t& b3) {
   const uint32_t x = __byte_perm(w[0], w[1], 0x5140), y = __byte_perm(w[2], w[3], 0x5140);
+  const uint32_t z = __byte_perm(w[0], w[1], 0x7362), t = __byte_perm(w[2], w[3], 0x7362);
   b0 = __byte_perm(x, y, 0x5410);
   b1 = __byte_perm(x, y, 0x7632);
-  b2 = __byte_perm(__byte_perm(w[0], w[1], 0x0062), __byte_perm(w[2], w[3], 0x0062), 0x5410);
+  b2 = __byte_perm(z, t, 0x5410);
+  b3 = __byte_perm(z, t, 0x7632);
 }
 
 // As mbar_wait_bounded, for waits that are often long: the hardware may suspend
@@ -499,6 +506,8 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     // ---------------- softmax: a token's scores -> weights ----------------
     const int row = tid;  // smem row; tokens row (and row + 128 at d = 64) of the tile
     constexpr int TPR = C::TPR;
+    // The fixed point of P counts in 2^-24 / cw; what it is made for lies in [8, 16) / cw.
+    constexpr float kMost = 255.0f;
     float m[R], l[R], cw[R];
     float ks[TPR][NG], vs[TPR][NG];
     bool fresh = true;
@@ -585,27 +594,24 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
               const float x = s[h][r] - m[r];
               p[r] = ex2(x);
               l[r] += p[r];
-              over = over || x > 7.0f || p[r] * vmax[h] * cw[r] > 127.0f;
+              over = over || x > 7.0f || p[r] * vmax[h] * cw[r] > kMost;
             }
           }
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
-            constexpr int NB = 3 * R / 4, NBR = (NB + 3) / 4 * 4;
-            uint32_t w[R], b[NBR];
-#pragma unroll
-            for (int r = NB; r < NBR; ++r) b[r] = 0u;
+            uint32_t w[R], b[R];
 #pragma unroll
             for (int r = 0; r < R; ++r)
-              w[r] = __float_as_uint(fmaf(p[r] * vs[h][j], cw[r] * 65536.0f, 8388608.0f));
+              w[r] = __float2uint_rn(p[r] * vs[h][j] * (cw[r] * 16777216.0f));
 #pragma unroll
             for (int r = 0; r < R / 4; ++r)
-              pd_slices(w + 4 * r, b[r], b[R / 4 + r], b[R / 2 + r]);
+              pd_slices(w + 4 * r, b[r], b[R / 4 + r], b[R / 2 + r], b[3 * R / 4 + r]);
             // row of NP bytes, a run of PW for each of its tokens; 16-byte pieces swizzled
             const uint32_t base = pt + uint32_t(j * 128 + row) * C::NP;
             const uint32_t x =
                 C::NP == 32 ? (row >> 2) & 1 : (C::NP == 64 ? (row >> 1) & 3 : row & 7);
 #pragma unroll
-            for (int k = 0; k < NBR; k += 4)
+            for (int k = 0; k < R; k += 4)
               sts128(base + ((uint32_t(h * (C::PW / 16) + k / 4) ^ x) * 16), b[k], b[k + 1],
                      b[k + 2], b[k + 3]);
           }
@@ -631,6 +637,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
             if (lane == 0) sh.red[warp][r] = x;
           }
           named_sync(1, 128);
+          uint32_t moved = 0;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             float mn = m[r];
@@ -638,6 +645,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
             for (int w = 0; w < 4; ++w) mn = fmaxf(mn, sh.red[w][r]);
             const float f = ex2(m[r] - mn);
             l[r] *= f;
+            if (fresh || mn > m[r]) moved |= 1u << r;
             m[r] = mn;
             float x = 0.0f;
 #pragma unroll
@@ -654,10 +662,13 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
             float x = 0.0f;
 #pragma unroll
             for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.red2[w][r]);
-            // the power of two that brings the largest into [1/2, 1)
-            const int ex = min(max(253 - int(__float_as_uint(x) >> 23), 1), 237);
-            cw[r] = __uint_as_float(uint32_t(ex) << 23);
-            if (row == 0) sh.icwcur[r] = __uint_as_float(uint32_t(254 - ex) << 23);
+            // the power of two that brings the largest into [8, 16); rows that need no
+            // other keep theirs
+            if ((moved >> r & 1u) || x * cw[r] > kMost) {
+              const int ex = min(max(257 - int(__float_as_uint(x) >> 23), 1), 225);
+              cw[r] = __uint_as_float(uint32_t(ex) << 23);
+              if (row == 0) sh.icwcur[r] = __uint_as_float(uint32_t(254 - ex) << 23);
+            }
           }
         }
         const bool over = weights();
@@ -668,7 +679,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
       __syncwarp();
       if (warp == 0 && lane < R) {  // what the accumulation needs to know of this tile
         sh.f[i & 3][lane] = slow ? sh.fcur[lane] : 1.0f;
-        sh.icw[i & 3][lane] = sh.icwcur[lane] * (1.0f / 1048576.0f);
+        sh.icw[i & 3][lane] = sh.icwcur[lane] * (1.0f / 268435456.0f);
         sh.m[i & 3][lane] = sh.mcur[lane];
       }
       if (e.ends) {
@@ -734,17 +745,25 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
         const int blk = D == 256 ? c * C::NGM + crd / (C::G > 128 ? 128 : C::G) : crd / C::G;
         const uint32_t at = tlane + 2 * C::SCOLS + (i % C::OBUF) * C::OCOLS +
                             uint32_t(blk * C::NP + half * C::PW);
-        uint32_t x0[R], x1[R], x2[R];
-        tmem_ld<R>(at, x0);
-        tmem_ld<R>(at + R, x1);
-        tmem_ld<R>(at + 2 * R, x2);
-        tmem_wait_ld();
+        // two slices of every row after the other two (16 rows: to save registers)
+        constexpr int RL = R > 8 ? 1 : 2;
+        float v[R];
+#pragma unroll
+        for (int k = 0; k < 4; k += 2 * RL) {
+          uint32_t x[2 * RL * R];
+          tmem_ld<2 * RL * R>(at + k * R, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 2 * RL; j += 2)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const float two = float(int(x[(j + 1) * R + r]) * 256 + int(x[j * R + r]));
+              v[r] = j + k == 0 ? two : fmaf(two, 65536.0f, v[r]);
+            }
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r)
-          if (r < rows) {
-            const float v = fmaf(float(int(x2[r])), 65536.0f, float(int(x1[r]) * 256 + int(x0[r])));
-            acc[c][r] = fmaf(v, sh.icw[i & 3][r], acc[c][r] * sh.f[i & 3][r]);
-          }
+          if (r < rows) acc[c][r] = fmaf(v[r], sh.icw[i & 3][r], acc[c][r] * sh.f[i & 3][r]);
       }
       float lsum = 0.0f, mref = 0.0f;
       if (e.ends && lane < R) {  // of query row `lane`

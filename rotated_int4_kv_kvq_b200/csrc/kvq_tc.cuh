@@ -26,12 +26,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]);
 #define KVQ_R4(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
 #define KVQ_R16(i) KVQ_R4(i), KVQ_R4(i + 4), KVQ_R4(i + 8), KVQ_R4(i + 12)
 template <>
-__device__ __forceinline__ void tmem_ld<4>(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : KVQ_R4(0)
-               : "r"(addr));
-}
-template <>
 __device__ __forceinline__ void tmem_ld<8>(uint32_t addr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : KVQ_R4(0), KVQ_R4(4)

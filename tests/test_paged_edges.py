@@ -8,8 +8,8 @@ import torch
 
 import oracle.kvq_oracle as O
 from rotated_int4_kv_kvq_b200 import workloads as W
-from test_paged import (BOTH, attend_tolerance, gen, kvq, make_batch, make_pool, np64,
-                         poison, rows, run_attend)  # noqa: F401
+from test_paged import (BOTH, attend_tolerance, check_large, gen, kvq, make_batch,
+                         make_pool, np64, poison, rows, run_attend)  # noqa: F401
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:invalid value:RuntimeWarning")]
 
@@ -108,3 +108,30 @@ def test_attend_pages_before_the_window(kvq, kind, d, group, nq, page, news, len
     cu = np.concatenate([[0], np.cumsum(news)]).tolist()
     q = rows(gen(nq), cu[-1], 2 * nq, d, torch.float16) * 0.25
     run_attend(kvq, cache, q, cu, lens, table, window=window)
+
+
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("levels", [(16.5, 17.5), (20.0,), (14.0, 19.0)])
+def test_attend_one_token_long_faint_tail(kvq, d, group, levels):
+    """One early token outweighs each of the others by 2^14 to 2^20, all of them
+    together weigh up to half as much as it."""
+    n, seqs, heads, page = 16000, 48, 4, 64
+    cache = make_pool(kvq, 8, n // page, heads, page, d, group, 0)
+    # every key points the way of the first, every value but the first is the second's
+    for t in (cache.k_packed, cache.k_scales, cache.v_packed, cache.v_scales):
+        t[:, :, 2:] = t[:1, :, 1:2]
+        t[1:, :, :2] = t[:1, :, 1:2]
+    cache.k_packed[:] = cache.k_packed[:1, :, :1].clone()
+    cache.k_scales[:] = cache.k_scales[:1, :, :1].clone()
+    signs = cache.signs.cpu().numpy()
+    key = O.dequant_rotated_f64(cache.k_packed[0, :, 0].cpu().numpy(),
+                                cache.k_scales[0, :, 0].cpu().numpy(), signs, 0, group)
+    top = 24.0  # score of the first token, the others 0 to 24 log 2 below
+    q = torch.from_numpy(top * d ** 0.5 * key / (key ** 2).sum(-1, keepdims=True)).cuda().half()
+    step = 1 - torch.tensor(levels, device="cuda", dtype=torch.float64) * np.log(2) / top
+    f = step[torch.arange(n, device="cuda") % len(levels)].float().reshape(n // page, 1, page, 1)
+    first = cache.k_scales[0, :, 0].clone()
+    cache.k_scales.mul_(f)
+    cache.k_scales[0, :, 0] = first
+    table = torch.arange(n // page, device="cuda", dtype=torch.int32).repeat(seqs, 1)
+    check_large(kvq, cache, q[None].repeat(seqs, 1, 1), list(range(seqs + 1)), [n] * seqs, table)
