@@ -394,7 +394,8 @@ KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtyp
  * window, t > p - window.  With K_t, V_t as in kvq_attend_decode, query head
  * h of that token and KV head h / n_q:
  *   s_t = sm_scale <q, K_t>,  out = sum_t softmax(s)_t V_t, rounded to dtype.
- * A token that attends no row gets zeros.  Rows of out that belong to no
+ * A token that attends no row gets zeros; one whose query holds a NaN or an
+ * infinity gets NaN (if it attends any).  Rows of out that belong to no
  * sequence are left as they were.  Products run on the tensor cores with fp32
  * (or exact integer) sums.  Up to 16 query rows of a sequence and KV head
  * (max_q_len * n_q): queries in 15-bit fixed point (2^-15 of the largest rotated

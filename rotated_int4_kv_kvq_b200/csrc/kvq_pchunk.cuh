@@ -154,10 +154,12 @@ __device__ __forceinline__ void regs_dec() {
 
 // Factor for a row whose largest rotated value is `top`: a power of two that
 // brings it into [2^8, 2^9), far from fp16's smallest and largest, with the sign
-// of the softmax scale; `back` undoes it and applies the scale.
+// of the softmax scale; `back` undoes it and applies the scale.  A row with an
+// infinity gets NaN: products of infinities alone could come out as "attends nothing".
 __device__ __forceinline__ float pc_scale(float top, float qscale, float& back) {
   const int e = min(max(int(__float_as_uint(top) >> 23), 20), 234);
   back = __uint_as_float(uint32_t(e - 8) << 23) * fabsf(qscale);  // 2^(e - 135)
+  if (!(top < INFINITY)) back = __uint_as_float(0x7FFFFFFFu);
   const float mul = __uint_as_float(uint32_t(262 - e) << 23);
   return qscale < 0.0f ? -mul : mul;
 }
@@ -785,7 +787,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         float* slot = part_slot<D, M>(a, blockIdx.x, began_here ? 1 : 0);
         const int r0 = x * 128 + w4 * 32;  // first row in the item
         if (!complete && lane < nr) slot[r0 + lane] = m, slot[M + r0 + lane] = l;
-        const float fin = complete ? (l > 0.0f ? unit / l : 0.0f) : unit;
+        const float fin = complete ? (l != 0.0f ? unit / l : 0.0f) : unit;
         if constexpr (D <= 128) {
           f2 Y[D / 2];
           // (the kappa of either rotation's inverse, 1 for a partial result)

@@ -147,7 +147,8 @@ __device__ __forceinline__ constexpr int pd_dim(int b) {
 }
 
 // Rotates one query row and writes its two slices; returns (in every lane) the
-// factor that turns integer sums into log2 scores.
+// factor that turns integer sums into log2 scores: NaN for a row that is not finite,
+// which integers cannot say.
 template <class C, int ROT>
 __device__ __forceinline__ float pd_query(const PagedAttnArgs& a, const uint16_t* row, uint8_t* sq,
                                           int r, int lane) {
@@ -166,11 +167,16 @@ __device__ __forceinline__ float pd_query(const PagedAttnArgs& a, const uint16_t
   float Y[P::W];
   wide_rotate_fwd<C::D, ROT>(z, L, Y);
   float top = 0.0f;
+  bool finite = true;
 #pragma unroll
-  for (int w = 0; w < P::W; ++w) top = fmaxf(top, fabsf(Y[w]));
+  for (int w = 0; w < P::W; ++w) {
+    top = fmaxf(top, fabsf(Y[w]));
+    finite = finite && fabsf(Y[w]) < INFINITY;
+  }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  const float inv = top > 0.0f ? 16256.0f / top : 0.0f;  // 127 * 128
+  finite = __all_sync(kFull, finite);
+  const float inv = finite && top > 0.0f ? 16256.0f / top : 0.0f;  // 127 * 128
   const int n0 = r, n1 = C::R + r;                        // columns of the slices
 #pragma unroll
   for (int w = 0; w < P::W; ++w) {
@@ -181,6 +187,7 @@ __device__ __forceinline__ float pd_query(const PagedAttnArgs& a, const uint16_t
     base[n0 * 128 + (in ^ ((n0 & 7) << 4))] = uint8_t(hi);
     base[n1 * 128 + (in ^ ((n1 & 7) << 4))] = uint8_t(lo);
   }
+  if (!finite) return __uint_as_float(0x7FFFFFFFu);
   return top * (1.0f / 16256.0f) * P::KAPPA * a.qscale * (1.0f / 16.0f);
 }
 
@@ -797,7 +804,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
           return v;
         };
         if (complete) {
-          const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
+          const float inv = ls != 0.0f ? 1.0f / ls : 0.0f;
           uint16_t* dst = out_row(a, e.c0, e.head, e.row0 + r);
           float Y[D / 32];
           if (a.rot == kRotSRFT) {
@@ -887,7 +894,7 @@ __global__ void __launch_bounds__(32 * RPB * WPR) kvq_paged_join_kernel(const Pa
     }
   }
   if (!there) return;
-  const float inv = l > 0.0f ? Wide<D, ROT>::KAPPA / l : 0.0f;
+  const float inv = l != 0.0f ? Wide<D, ROT>::KAPPA / l : 0.0f;  // (a NaN stays one)
 #pragma unroll
   for (int w = 0; w < W; ++w) Y[w] *= inv;
   pd_store<D, ROT>(a, Y, L, out_row(a, j.c0, j.head, j.row0 + r));

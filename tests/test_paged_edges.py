@@ -135,3 +135,30 @@ def test_attend_one_token_long_faint_tail(kvq, d, group, levels):
     cache.k_scales[0, :, 0] = first
     table = torch.arange(n // page, device="cuda", dtype=torch.int32).repeat(seqs, 1)
     check_large(kvq, cache, q[None].repeat(seqs, 1, 1), list(range(seqs + 1)), [n] * seqs, table)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("rot", [O.SRFT, O.SRHT])
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("max_q", [1, 1000])
+def test_attend_queries_not_finite(kvq, dtype, rot, d, group, max_q):
+    """A query with a NaN or an infinity gives NaN, whichever kernel takes it; its
+    neighbours, and tokens that attend nothing, are what they were."""
+    lens, nq = [900, 1, 0, 40], 4
+    cache = make_pool(kvq, d, 70, 2, 16, d, group, rot)
+    table = make_batch(cache, 9, lens)
+    q = rows(gen(4), 4, 2 * nq, d, dtype) * 0.25
+    args = (cache, torch.arange(5, device="cuda", dtype=torch.int32),
+            torch.tensor(lens, device="cuda", dtype=torch.int32), table)
+    want = kvq.kvq_paged_attend(q, *args, max_q_len=max_q)
+    bad = [(0, 0, float("nan")), (0, 5, float("inf")), (1, 2, -float("inf")), (1, 7, float("inf")),
+           (1, 4, float("nan")), (2, 3, float("nan")), (2, 1, float("inf"))]
+    for t, h, x in bad:
+        q[t, h, (7 * h + 3) % d] = x
+        if t != 2:
+            want[t, h] = float("nan")
+    got = kvq.kvq_paged_attend(q, *args, max_q_len=max_q)
+    assert kvq.kvq_device_status() == 0
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(), want.nan_to_num())
+    assert (got[2] == 0).all()
