@@ -374,16 +374,26 @@ def paged_rows(cu_q: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tenso
                page_size: int, n_tokens: int):
     """Positions [n_tokens] int32 and slots [n_tokens] int64 of the new tokens
     that cu_q, kv_len (after the append) and page_table describe, for
-    kvq_qk_norm_rope and kvq_paged_append; -1 for tokens of no sequence.  The
-    same for every layer: computed once a step, on the device, without a
-    synchronization."""
+    kvq_qk_norm_rope and kvq_paged_append; -1 for tokens of no sequence or
+    before position 0.  A token whose page the table does not have (past its
+    end, or a negative entry) gets a slot past every pool, which the append
+    skips and reports.  The same for every layer: computed once a step, on the
+    device, without a synchronization."""
     tok = torch.arange(n_tokens, device=cu_q.device)
-    seq = torch.searchsorted(cu_q[1:], tok, right=True).clamp_(max=kv_len.shape[0] - 1)
-    here = (tok >= cu_q[0]) & (tok < cu_q[-1])
-    pos = torch.where(here, kv_len[seq].long() - cu_q[1:][seq] + tok, -1)
-    page = page_table[seq, (pos // page_size).clamp_(0, page_table.shape[1] - 1)].long()
-    slots = torch.where(pos >= 0, page * page_size + pos % page_size, -1)
-    return pos.int(), slots
+    n_seqs, max_pages = page_table.shape
+    if n_seqs == 0:
+        return torch.full_like(tok, -1, dtype=torch.int32), torch.full_like(tok, -1)
+    seq = torch.searchsorted(cu_q[1:], tok, right=True).clamp_(max=n_seqs - 1)
+    end = cu_q[1:][seq]
+    here = (tok >= cu_q[seq]) & (tok < end)
+    pos = torch.where(here, kv_len[seq].long() - end + tok, -1)
+    col = pos // page_size
+    if max_pages:
+        page = page_table[seq, col.clamp(0, max_pages - 1)].long()
+    else:
+        page = torch.full_like(tok, -1)
+    slots = torch.where((col < max_pages) & (page >= 0), page * page_size + pos % page_size, 1 << 62)
+    return pos.int(), torch.where(pos >= 0, slots, -1)
 
 
 class PagedCache:

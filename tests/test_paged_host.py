@@ -166,6 +166,58 @@ def test_paged_rows(kvq):
     assert slots.tolist() == [33, 34, 35, 112, 113, 114, 115, -1, -1] and slots.dtype == torch.int64
 
 
+NOWHERE = 1 << 62  # past every pool: the append skips and reports it
+
+
+def test_paged_rows_past_the_table(kvq):
+    """A token whose page the table does not have must not land on another's row."""
+    i32 = dict(dtype=torch.int32)
+    # two pages of 16: positions 32 and 33 have none
+    pos, slots = kvq.paged_rows(torch.tensor([0, 3, 4], **i32), torch.tensor([34, 40], **i32),
+                                torch.tensor([[5, 9], [3, 4]], **i32), 16, 5)
+    assert pos.tolist() == [31, 32, 33, 39, -1]
+    assert slots.tolist() == [9 * 16 + 15, NOWHERE, NOWHERE, NOWHERE, -1]
+    # a page that was never given, or was released
+    pos, slots = kvq.paged_rows(torch.tensor([0, 3], **i32), torch.tensor([17], **i32),
+                                torch.tensor([[2, -1]], **i32), 16, 3)
+    assert pos.tolist() == [14, 15, 16] and slots.tolist() == [46, 47, NOWHERE]
+    # more new tokens than rows: those before position 0 have none
+    pos, slots = kvq.paged_rows(torch.tensor([0, 3], **i32), torch.tensor([2], **i32),
+                                torch.tensor([[2]], **i32), 16, 3)
+    assert pos.tolist()[1:] == [0, 1] and pos[0] < 0 and slots.tolist() == [-1, 32, 33]
+
+
+def test_paged_rows_of_nothing(kvq):
+    """A padded batch without sequences, a table without pages, no tokens."""
+    i32 = dict(dtype=torch.int32)
+    pos, slots = kvq.paged_rows(torch.zeros(1, **i32), torch.zeros(0, **i32),
+                                torch.zeros((0, 4), **i32), 16, 3)
+    assert pos.tolist() == [-1] * 3 and pos.dtype == torch.int32
+    assert slots.tolist() == [-1] * 3 and slots.dtype == torch.int64
+    pos, slots = kvq.paged_rows(torch.tensor([0, 1], **i32), torch.tensor([1], **i32),
+                                torch.zeros((1, 0), **i32), 16, 2)
+    assert pos.tolist() == [0, -1] and slots.tolist() == [NOWHERE, -1]
+    pos, slots = kvq.paged_rows(torch.tensor([0, 0], **i32), torch.tensor([7], **i32),
+                                torch.zeros((1, 2), **i32), 16, 0)
+    assert pos.shape == slots.shape == (0,)
+
+
+def test_paged_rows_offsets_out_of_order(kvq):
+    """Only a sequence that holds a token says where it goes."""
+    i32 = dict(dtype=torch.int32)
+    for cu in ([0, 6, 2, 8], [3, 1, 8, 8], [0, 9, 4, 2], [-4, 2, 4, 6]):
+        lens, table = [20, 20, 20], [[1, 2], [3, 4], [5, 6]]
+        pos, slots = kvq.paged_rows(torch.tensor(cu, **i32), torch.tensor(lens, **i32),
+                                    torch.tensor(table, **i32), 16, 8)
+        for t, (p, s) in enumerate(zip(pos.tolist(), slots.tolist())):
+            may = {(-1, -1)}
+            for b, e, n, row in zip(cu, cu[1:], lens, table):
+                if b <= t < e:
+                    q = n - e + t
+                    may.add((q, row[q // 16] * 16 + q % 16) if q >= 0 else (q, -1))
+            assert (p, s) in may
+
+
 def test_oracle_norm_rope_turns_pairs():
     """A rotation keeps each pair's length and adds angles: position p on top
     of position p' is p + p'."""
