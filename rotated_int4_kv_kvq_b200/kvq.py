@@ -400,7 +400,8 @@ class PagedCache:
     """The int4 K/V cache of one layer in pages: k_packed, v_packed
     [pages, H, page_size, d/2] u8, k_scales, v_scales [pages, H, page_size,
     d/group] f32, the sign vector [d] i8 and the rotation.  A page row is a row
-    of kvq_rot_quant_fwd."""
+    of kvq_rot_quant_fwd.  The fields are fixed (calls use the tensors' addresses):
+    other tensors want another PagedCache."""
 
     __slots__ = ("k_packed", "k_scales", "v_packed", "v_scales", "signs", "rot", "n_pages",
                  "n_kv_heads", "page_size", "d", "group", "device", "c", "ref")
@@ -420,16 +421,20 @@ class PagedCache:
         _check(k_scales, "k_scales", torch.float32, shape)
         _check(v_scales, "v_scales", torch.float32, shape)
         _check(signs, "signs", torch.int8, (d,))
-        self.device = _one_device((k_packed, k_scales, v_packed, v_scales, signs))
-        self.n_pages, self.n_kv_heads, self.page_size = pages, heads, page
-        self.d, self.group, self.rot = d, group, rot
-        self.k_packed, self.k_scales = k_packed, k_scales
-        self.v_packed, self.v_scales = v_packed, v_scales
-        self.signs = signs
-        self.c = _PagedCacheC(k_packed.data_ptr(), v_packed.data_ptr(), k_scales.data_ptr(),
-                              v_scales.data_ptr(), pages, heads, page, d, group, signs.data_ptr(),
-                              rot)
-        self.ref = ctypes.addressof(self.c)
+        dev = _one_device((k_packed, k_scales, v_packed, v_scales, signs))
+        c = _PagedCacheC(k_packed.data_ptr(), v_packed.data_ptr(), k_scales.data_ptr(),
+                         v_scales.data_ptr(), pages, heads, page, d, group, signs.data_ptr(), rot)
+        fields = dict(k_packed=k_packed, k_scales=k_scales, v_packed=v_packed, v_scales=v_scales,
+                      signs=signs, rot=rot, n_pages=pages, n_kv_heads=heads, page_size=page, d=d,
+                      group=group, device=dev, c=c, ref=ctypes.addressof(c))
+        for name, value in fields.items():
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"the fields of a PagedCache are fixed ({name!r}): make another one")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"the fields of a PagedCache are fixed ({name!r}): make another one")
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, d: int, group: int,

@@ -162,3 +162,15 @@ def test_attend_queries_not_finite(kvq, dtype, rot, d, group, max_q):
     assert torch.equal(got.isnan(), want.isnan())
     assert torch.equal(got.nan_to_num(), want.nan_to_num())
     assert (got[2] == 0).all()
+
+
+def test_cache_fields_are_fixed(kvq):
+    """The addresses that calls use are those of the tensors the cache shows."""
+    signs = torch.from_numpy(W.make_signs(64)).cuda()
+    cache = kvq.PagedCache.empty(4, 2, 16, 64, 32, signs)
+    for name in ("k_packed", "v_scales", "signs", "rot", "n_pages", "group", "c", "ref", "other"):
+        with pytest.raises(AttributeError, match="PagedCache"):
+            setattr(cache, name, getattr(cache, name, None))
+    with pytest.raises(AttributeError, match="PagedCache"):
+        del cache.k_packed
+    assert cache.k_packed.data_ptr() == cache.c.k_packed
