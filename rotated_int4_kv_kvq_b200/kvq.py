@@ -440,6 +440,9 @@ class PagedCache:
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, d: int, group: int,
               signs: torch.Tensor, rot: int = SRFT) -> "PagedCache":
         """A pool of n_pages uninitialized pages on the device of `signs`."""
+        if group < 1 or d % group != 0:
+            raise ValueError(f"group {group} does not divide d = {d}")
+
         def codes():
             return torch.empty((n_pages, n_kv_heads, page_size, d // 2), dtype=torch.uint8,
                                device=signs.device)

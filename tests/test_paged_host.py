@@ -148,6 +148,13 @@ def test_binding_checks_before_launch(kvq):
         kvq.PagedCache.empty(2, 1, 16, 64, 32, torch.ones(64, dtype=torch.int8))
 
 
+@pytest.mark.parametrize("group", [48, 40, 0, -32, 96, 100, 256])
+def test_cache_of_no_such_group(kvq, group):
+    """A group that does not divide d is refused, not replaced by one that does."""
+    with pytest.raises(ValueError, match="group"):
+        kvq.PagedCache.empty(4, 2, 16, 128, group, torch.ones(128, dtype=torch.int8))
+
+
 def test_rope_table(kvq):
     t = kvq.rope_table(5000, 32, 500000.0, device="cpu").numpy()
     for p in (0, 1, 777, 4999):
