@@ -431,6 +431,8 @@ class PagedCache:
             object.__setattr__(self, name, value)
 
     def __setattr__(self, name, value):
+        if getattr(self, name, None) is value and name in self.__slots__:
+            return  # cache.k_scales *= 2 works in place, then assigns what is there
         raise AttributeError(f"the fields of a PagedCache are fixed ({name!r}): make another one")
 
     def __delattr__(self, name):

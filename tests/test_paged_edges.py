@@ -168,9 +168,11 @@ def test_cache_fields_are_fixed(kvq):
     """The addresses that calls use are those of the tensors the cache shows."""
     signs = torch.from_numpy(W.make_signs(64)).cuda()
     cache = kvq.PagedCache.empty(4, 2, 16, 64, 32, signs)
+    other = kvq.PagedCache.empty(9, 4, 32, 128, 128, torch.from_numpy(W.make_signs(128)).cuda(), 1)
     for name in ("k_packed", "v_scales", "signs", "rot", "n_pages", "group", "c", "ref", "other"):
         with pytest.raises(AttributeError, match="PagedCache"):
-            setattr(cache, name, getattr(cache, name, None))
+            setattr(cache, name, getattr(other, name, None))
     with pytest.raises(AttributeError, match="PagedCache"):
         del cache.k_packed
+    cache.k_scales *= 2.0  # in place
     assert cache.k_packed.data_ptr() == cache.c.k_packed
