@@ -516,6 +516,12 @@ def _check_tokens(t: torch.Tensor, name: str, dtype, shape) -> int:
     return st if tokens > 1 else heads * d  # the stride of a single token says nothing
 
 
+def _int32(x) -> int:
+    """A whole number of rows or tokens for an int32 argument: beyond it as good
+    as the largest, below 0 refused by the call.  (ctypes keeps the low 32 bits.)"""
+    return max(-1, min(int(x), (1 << 31) - 1))
+
+
 def _rope(positions, cos_sin, interleaved, eps, n_tokens):
     """(address of positions, kvq_rope) of a call."""
     if cos_sin is None:
@@ -636,6 +642,7 @@ def kvq_paged_attend(q: torch.Tensor, cache: PagedCache, cu_q: torch.Tensor,
         outs = h * d
     else:
         outs = _check_tokens(out, "out", dt, shape)
+    max_q_len, window = _int32(max_q_len), _int32(window)
     n_seqs = kv_len.shape[0]
     max_pages = page_table.shape[-1]
     _check(kv_len, "kv_len", torch.int32, (n_seqs,))

@@ -164,6 +164,23 @@ def test_attend_queries_not_finite(kvq, dtype, rot, d, group, max_q):
     assert (got[2] == 0).all()
 
 
+@pytest.mark.parametrize("news", [[1, 1], [40, 30]])
+def test_attend_window_past_32_bits(kvq, news):
+    """A window of any size is a whole number of rows, not its low 32 bits."""
+    cache = make_pool(kvq, 2, 20, 1, 16, 64, 64, 0)
+    lens = [77, 150]
+    table = make_batch(cache, 7, lens)
+    q = rows(gen(3), sum(news), 2, 64, torch.float16) * 0.25
+    args = (q, [0, news[0], sum(news)], lens, table)
+    want = run_attend(kvq, cache, *args)
+    for window in (2 ** 31, 2 ** 32 + 3, 2 ** 63 - 1, 2 ** 70):
+        assert torch.equal(run_attend(kvq, cache, *args, window=window), want)
+    assert torch.equal(run_attend(kvq, cache, *args, max_q=2 ** 40), want) or max(news) == 1
+    for kw in (dict(window=-1), dict(window=-2 ** 32), dict(max_q=0), dict(max_q=-2 ** 32 + 1)):
+        with pytest.raises(kvq.KVQError, match="BAD_SIZE"):
+            run_attend(kvq, cache, *args, **kw)
+
+
 def test_cache_fields_are_fixed(kvq):
     """The addresses that calls use are those of the tensors the cache shows."""
     signs = torch.from_numpy(W.make_signs(64)).cuda()
