@@ -336,9 +336,10 @@ typedef struct {
  *   q          [n_tokens][n_heads][d], token stride q_stride (read)
  *   k          [n_tokens][n_k_heads][d], token stride k_stride (read);
  *              NULL with n_k_heads == 0: queries only
- *   positions  [n_tokens] int32 (NULL without a rotation).  A token at a
- *              negative position is padding: its rows are left as they were.
- *              So are those of a position >= n_pos (KVQ_ERR_BAD_INDEX).
+ *   positions  [n_tokens] int32 (may be NULL without a rotation).  A token at
+ *              a negative position is padding: its rows are left as they were.
+ *              So are, with a rotation, those of a position >= n_pos
+ *              (KVQ_ERR_BAD_INDEX).
  *   q_weight, k_weight  [d] fp32, 16-byte aligned, or NULL: no norm
  *   q_out, k_out  as q and k, token strides q_out_stride, k_out_stride
  *              (written); rounded once, to dtype.  They may be q and k

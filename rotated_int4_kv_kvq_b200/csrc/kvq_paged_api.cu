@@ -89,7 +89,7 @@ kvq_status kvq_qk_norm_rope(const void* q, const void* k, kvq_dtype dtype, int64
   if (!q || !q_out || (n_k_heads > 0 && (!k || !k_out))) return KVQ_ERR_NULL;
   if (rope == nullptr && (q_weight || k_weight)) return KVQ_ERR_NULL;
   if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(k_out, 16) ||
-      !aligned(q_weight, 16) || !aligned(k_weight, 16))
+      !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 4))
     return KVQ_ERR_MISALIGNED;
   kvq::NormRopeArgs a = {};
   if (kvq_status s = check_rope(rope, positions, d, &a.rope)) return s;

@@ -58,10 +58,14 @@ __global__ void __launch_bounds__(kRopeThreads) kvq_norm_rope_kernel(const NormR
   const int half = a.rope.rot_dim / 2;
   float cs[8], sn[8];
   int src = lane;  // lane of the rotation partner
+  int64_t pos = 0;
+  if (a.positions != nullptr) {
+    pos = __ldg(a.positions + tok);
+    if (pos < 0) return;  // padding
+  }
   if (a.rope.cos_sin != nullptr) {
-    const int64_t pos = __ldg(a.positions + tok);
-    if (pos < 0 || pos >= a.rope.n_pos) {
-      if (pos >= 0 && lane == 0) flag_bad_index(status);
+    if (pos >= a.rope.n_pos) {
+      if (lane == 0) flag_bad_index(status);
       return;
     }
     const float* row = a.rope.cos_sin + pos * a.rope.rot_dim;

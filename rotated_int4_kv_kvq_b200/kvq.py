@@ -523,17 +523,20 @@ def _int32(x) -> int:
 
 
 def _rope(positions, cos_sin, interleaved, eps, n_tokens):
-    """(address of positions, kvq_rope) of a call."""
+    """(address of positions or None, kvq_rope) of a call."""
+    pos = None
+    if positions is not None:
+        _check(positions, "positions", torch.int32, (n_tokens,))
+        pos = positions.data_ptr()
     if cos_sin is None:
-        return None, _RopeC(None, 0, 0, 0, eps)
+        return pos, _RopeC(None, 0, 0, 0, eps)
     if positions is None:
         raise ValueError("a rotation needs positions")
-    _check(positions, "positions", torch.int32, (n_tokens,))
     if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be a table [positions, rot_dim]")
     n_pos, rot_dim = shape = cos_sin.shape
     _check(cos_sin, "cos_sin", torch.float32, shape)
-    return positions.data_ptr(), _RopeC(cos_sin.data_ptr(), n_pos, rot_dim, bool(interleaved), eps)
+    return pos, _RopeC(cos_sin.data_ptr(), n_pos, rot_dim, bool(interleaved), eps)
 
 
 def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *,
@@ -546,7 +549,8 @@ def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *,
     (table cos_sin [positions, rot_dim] f32, see rope_table; none without a
     table) of queries q [T, Hq, d] and keys k [T, Hk, d], fp16 or bf16, in one
     pass.  Returns (q_out, k_out), allocated when not given; they may be q and
-    k themselves.  Rows of tokens at negative positions are left as they were."""
+    k themselves.  Rows of tokens at negative positions are left as they were,
+    with or without a rotation."""
     t, hq, d = shape = q.shape
     dt = q.dtype
     qs = _check_tokens(q, "q", dt, shape)
@@ -574,8 +578,7 @@ def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *,
         _check(k_weight, "k_weight", torch.float32, (d,))
         kwp = k_weight.data_ptr()
     pos, rope = _rope(positions, cos_sin, interleaved, eps, t)
-    dev = _one_device((q, k, positions if pos is not None else None, cos_sin, q_weight, k_weight,
-                       q_out, k_out))
+    dev = _one_device((q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out))
     _call("kvq_qk_norm_rope", dev, stream,
           (q.data_ptr(), kp, DTYPES[dt], t, hq, hk, d, qs, ks, pos, qwp, kwp,
            ctypes.addressof(rope), q_out.data_ptr(), kop, qos, kos))
@@ -609,8 +612,7 @@ def kvq_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cach
         _check(v_hat, "v_hat", dt, shape)
         vh = v_hat.data_ptr()
     pos, rope = _rope(positions, cos_sin, interleaved, eps, t)
-    dev = _one_device((cache.signs, k, v, slots, positions if pos is not None else None, cos_sin,
-                       k_weight, k_hat, v_hat))
+    dev = _one_device((cache.signs, k, v, slots, positions, cos_sin, k_weight, k_hat, v_hat))
     _call("kvq_paged_append", dev, stream,
           (k.data_ptr(), v.data_ptr(), DTYPES[dt], t, ks, vs, slots.data_ptr(), pos, kw,
            ctypes.addressof(rope), cache.ref, kh, vh))

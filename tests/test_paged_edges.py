@@ -8,8 +8,8 @@ import torch
 
 import oracle.kvq_oracle as O
 from rotated_int4_kv_kvq_b200 import workloads as W
-from test_paged import (BOTH, attend_tolerance, check_large, gen, kvq, make_batch,
-                         make_pool, np64, poison, rows, run_attend)  # noqa: F401
+from test_paged import (BOTH, attend_tolerance, check_large, check_rounded, gen, kvq,
+                         make_batch, make_pool, np64, poison, rows, run_attend)  # noqa: F401
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:invalid value:RuntimeWarning")]
 
@@ -162,6 +162,24 @@ def test_attend_queries_not_finite(kvq, dtype, rot, d, group, max_q):
     assert torch.equal(got.isnan(), want.isnan())
     assert torch.equal(got.nan_to_num(), want.nan_to_num())
     assert (got[2] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_norm_without_rotation_skips_padding(kvq, d):
+    """Rows of tokens at negative positions stay, also where only a norm is asked for."""
+    q, k = rows(gen(1), 6, 3, d, torch.float16), rows(gen(2), 6, 1, d, torch.float16)
+    w = torch.randn(d, generator=gen(3), device="cuda")
+    pos = torch.tensor([4, -1, 2 ** 31 - 1, 0, -7, -2 ** 31], device="cuda", dtype=torch.int32)
+    qo, ko = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    kvq.kvq_qk_norm_rope(q, k, positions=pos, q_weight=w, k_weight=w, q_out=qo, k_out=ko)
+    assert kvq.kvq_device_status() == 0  # without a table no position is outside it
+    for x, o in ((q, qo), (k, ko)):
+        assert (o[[1, 4, 5]] == 7.0).all()
+        n = O.norm_rope(np64(x), np64(w), None, None)
+        check_rounded(o[[0, 2, 3]], n[[0, 2, 3]], torch.float16,
+                      np.abs(n).max(axis=-1, keepdims=True)[[0, 2, 3]])
+    with pytest.raises(TypeError, match="int32"):
+        kvq.kvq_qk_norm_rope(q, positions=pos.long(), q_weight=w)
 
 
 @pytest.mark.parametrize("news", [[1, 1], [40, 30]])
