@@ -571,6 +571,8 @@ def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *,
         else:
             kos = _check_tokens(k_out, "k_out", dt, kshape)
         kp, kop = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     if q_weight is not None:
         _check(q_weight, "q_weight", torch.float32, (d,))
         qwp = q_weight.data_ptr()

@@ -211,3 +211,10 @@ def test_cache_fields_are_fixed(kvq):
         del cache.k_packed
     cache.k_scales *= 2.0  # in place
     assert cache.k_packed.data_ptr() == cache.c.k_packed
+
+
+def test_key_output_without_keys(kvq):
+    """What would come back unwritten is refused."""
+    q, w = rows(gen(1), 3, 2, 64, torch.float16), torch.ones(64, device="cuda")
+    with pytest.raises(ValueError, match="k_out"):
+        kvq.kvq_qk_norm_rope(q, q_weight=w, k_out=torch.empty_like(q))
