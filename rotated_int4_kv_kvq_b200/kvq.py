@@ -477,15 +477,16 @@ def _enter(dev: int, stream):
     The context is None when the device is current already."""
     if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
         raise ValueError(f"stream is on {stream.device}, tensors on cuda:{dev}")
+    if stream is None:
+        raw = (_raw_current_stream(dev) if _raw_current_stream is not None
+               else torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
     guard = None
-    if dev != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():  # last: nothing after it can fail
         guard = torch.cuda.device(dev)
         guard.__enter__()
-    if stream is None:
-        if _raw_current_stream is not None:
-            return _raw_current_stream(dev), guard
-        stream = torch.cuda.current_stream(dev)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream), guard
+    return raw, guard
 
 
 def _call(fn: str, dev: int, stream, args) -> None:

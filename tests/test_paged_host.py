@@ -148,6 +148,29 @@ def test_binding_checks_before_launch(kvq):
         kvq.PagedCache.empty(2, 1, 16, 64, 32, torch.ones(64, dtype=torch.int8))
 
 
+def test_refused_stream_leaves_the_device(kvq, monkeypatch):
+    """A call that fails on its stream argument does not change the current device."""
+    entered = []
+
+    class Guard:
+        def __init__(self, dev):
+            pass
+
+        def __enter__(self):
+            entered.append(1)
+
+        def __exit__(self, *_):
+            entered.pop()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    with pytest.raises((TypeError, ValueError)):
+        kvq._enter(1, "no stream")
+    assert not entered
+    raw, guard = kvq._enter(1, 1234)
+    assert raw == 1234 and isinstance(guard, Guard) and entered == [1]
+    assert kvq._enter(0, 1234) == (1234, None)
+
+
 @pytest.mark.parametrize("group", [48, 40, 0, -32, 96, 100, 256])
 def test_cache_of_no_such_group(kvq, group):
     """A group that does not divide d is refused, not replaced by one that does."""
