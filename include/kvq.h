@@ -399,10 +399,13 @@ KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtyp
  * infinity gets NaN (if it attends any).  Rows of out that belong to no
  * sequence are left as they were.  Products run on the tensor cores with fp32
  * (or exact integer) sums.  Up to 16 query rows of a sequence and KV head
- * (max_q_len * n_q): queries in 15-bit fixed point (2^-15 of the largest rotated
- * value), weights times V scales in 32-bit (2^-28 of the largest).  More:
- * rotated queries and weights rounded to fp16, and with g < d the ratios of a
- * row's scales; a score is then off by at most 3 2^-12 sm_scale |q| |K_t|.
+ * (max_q_len * n_q): rotated queries in 15-bit fixed point, off by at most 1/32512
+ * of the row's largest value; weights times V scales in 32-bit, off by 2^-28 of the
+ * largest.  More: rotated queries, weights times V scales and, with g < d, the
+ * ratios of a row's K or V scales and their products with the codes rounded to
+ * fp16 (2^-11 of a value each).  A score is then off by at most 3.1 2^-11
+ * sm_scale |q| |K_t| (1.1 2^-11 with g = d), a weight times its V scale by 2^-11
+ * of itself or 2^-31 of the largest V scale that the token attends.
  *
  *   q          [n_tokens][n_kv_heads * n_q][d], token stride q_stride (read)
  *   out        same, token stride out_stride (written); must not overlap q

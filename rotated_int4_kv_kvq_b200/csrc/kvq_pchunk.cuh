@@ -7,7 +7,7 @@
 // (4 d flops a row and key) and by the 2^x of every score.
 //
 //   S = Q C_K^T      kind::f16, f32 accumulators: Q the rotated queries in fp16
-//                    (each row scaled by a power of two, error 2^-12 of a
+//                    (each row scaled by a power of two, error 2^-11 of a
 //                    value: as much as rounding a query to fp16 once), C_K the
 //                    codes, exact
 //   p = 2^(S s_K[t] c_row - m)      f32; the row's reference m moves only when
@@ -21,7 +21,8 @@
 //                    seen.  Scales lie in shared memory over their tile's power of
 //                    two; the difference of the exponents joins the reference m.
 // With several scales a row (g < d) a row's largest scale is kept apart in f32
-// and the codes are multiplied by the ratios s_j / s_max, rounded to fp16.
+// and the codes are multiplied by the ratios s_j / s_max: ratio and product are
+// rounded to fp16, 2^-11 each, so a score is off by three times that at most.
 //
 // A block holds 256 query rows (two tiles of 128; one at d = 256, where tensor
 // memory holds one): while the tensor cores work for one tile the other one's
@@ -639,7 +640,6 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         wait(sh.sdone[slot], NT == 2 ? used : i >> 1);
         wait(sh.scfull[i & 3], i >> 2);
         tc_fence_after();
-        const uint32_t ksa = smem_u32(sh.ks[i & 3]), vsa = smem_u32(sh.vs[i & 3]);
         // first and last position of the warp's rows decide on masks
         const int pf = __shfl_sync(kFull, pos, 0), pl = __shfl_sync(kFull, pos, 31);
         const bool whole = e.t0 + KT - 1 <= pf && (a.window == 0 || e.t0 > pl - a.window) &&

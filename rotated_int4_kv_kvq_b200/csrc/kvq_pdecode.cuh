@@ -14,7 +14,7 @@
 // operands by three logic operations.
 //   scores   S[t][n] = sum_i 16 c_K[t][i] Q[n][i]     kind::i8, s32
 //            Q: each rotated query in 15-bit fixed point, two 7-bit slices
-//            (error 2^-15 of its largest coordinate)
+//            (error 1/32512 of its largest coordinate)
 //   values   O[i][n] = sum_t 16 c_V[t][i] P[t][n]     kind::i8, s32
 //            P: weight times V scale in 32-bit fixed point, four 8-bit
 //            slices (error 2^-28 of the largest so far)
