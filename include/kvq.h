@@ -396,7 +396,7 @@ KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtyp
  * h of that token and KV head h / n_q:
  *   s_t = sm_scale <q, K_t>,  out = sum_t softmax(s)_t V_t, rounded to dtype.
  * A token that attends no row gets zeros; one whose query holds a NaN or an
- * infinity gets NaN (if it attends any).  Rows of out that belong to no
+ * infinity, or that attends a row with such a scale, gets NaN.  Rows of out that belong to no
  * sequence are left as they were.  Products run on the tensor cores with fp32
  * (or exact integer) sums.  Up to 16 query rows of a sequence and KV head
  * (max_q_len * n_q): rotated queries in 15-bit fixed point, off by at most 1/32512

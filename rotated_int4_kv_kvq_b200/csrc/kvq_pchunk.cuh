@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         for (int k = 0; k < NP; ++k) {
           uint32_t f = 0;
           if constexpr (NG > 1) {
-            const float x = sc[k * 32 / C::G] * inv;
+            const float x = top > 0.0f ? sc[k * 32 / C::G] * inv : 0.0f;
             f = float2_to_half2_bits(x, x);
           }
           const uint32_t words[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
@@ -537,18 +537,20 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         }
         fence_proxy_async_smem();
       };
+      // NaN if one is not finite: the operand is 0 then (another row's P of 0 has to
+      // stay one), and who attends the token gets NaN from its scale.
       auto largest = [](const float (&s)[NG]) {
-        float x = s[0];
+        float x = s[0], sum = s[0];
 #pragma unroll
-        for (int j = 1; j < NG; ++j) x = fmaxf(x, s[j]);
-        return x;
+        for (int j = 1; j < NG; ++j) x = fmaxf(x, s[j]), sum += s[j];
+        return fmaf(sum, 0.0f, x);
       };
       wait(sh.dfull[0], 0);
       load(0);
       for (int i = 0; i < n; ++i) {
         const float ktop = largest(ksc), vtop = largest(vsc);
         // the V scales of the tile under a power of two
-        float x = vtop;
+        float x = fmaxf(vtop, 0.0f);  // (of the finite ones)
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
         if (lane == 0) sh.wmax[i & 1][warp - C::W_DEQ] = x;
@@ -745,13 +747,15 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
 #pragma unroll
               for (int b = 0; b < 4; b += 2) {
                 const f2 kk = b == 0 ? mk2(k.x, k.y) : mk2(k.z, k.w);
-                const f2 vv = b == 0 ? mk2(v.x, v.y) : mk2(v.z, v.w);
+                f2 vv = b == 0 ? mk2(v.x, v.y) : mk2(v.z, v.w);
                 const f2 t = mul2(mk2(__uint_as_float(s[j + b]), __uint_as_float(s[j + b + 1])), kk);
                 const f2 z = fma2(t, rc2, nm2);
                 float z0 = lo2(z), z1 = hi2(z);
                 if constexpr (MASK) {
-                  if (!(sm >> (j + b) & 1u)) z0 = -INFINITY;
-                  if (!(sm >> (j + b + 1) & 1u)) z1 = -INFINITY;
+                  // (the scale too: what is hidden may be NaN)
+                  const bool s0 = sm >> (j + b) & 1u, s1 = sm >> (j + b + 1) & 1u;
+                  z0 = s0 ? z0 : -INFINITY, z1 = s1 ? z1 : -INFINITY;
+                  vv = mk2(s0 ? lo2(vv) : 0.0f, s1 ? hi2(vv) : 0.0f);
                 }
                 const f2 pp = mk2(ex2(z0), ex2(z1));
                 l2 = add2(l2, pp);

@@ -544,8 +544,15 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
           vs[h][j] = seen[h] ? sc[C::SC / 4 + j] : 0.0f;
         }
         vmax[h] = vs[h][0];
+        float sum = ks[h][0] + vs[h][0];
 #pragma unroll
-        for (int j = 1; j < NG; ++j) vmax[h] = fmaxf(vmax[h], vs[h][j]);
+        for (int j = 1; j < NG; ++j) {
+          vmax[h] = fmaxf(vmax[h], vs[h][j]);
+          sum += ks[h][j] + vs[h][j];
+        }
+        // A scale that is not finite makes the token's scores NaN, and with them the
+        // sums of those who attend it: integers could not say so.
+        ks[h][0] = fmaf(sum, 0.0f, ks[h][0]);
       }
       wait(sh.sdone[i & 1], i >> 1);
       tc_fence_after();

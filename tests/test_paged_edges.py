@@ -218,3 +218,34 @@ def test_key_output_without_keys(kvq):
     q, w = rows(gen(1), 3, 2, 64, torch.float16), torch.ones(64, device="cuda")
     with pytest.raises(ValueError, match="k_out"):
         kvq.kvq_qk_norm_rope(q, q_weight=w, k_out=torch.empty_like(q))
+
+
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("news,lens,window", [([1, 1], [300, 77], 0), ([4, 3], [300, 77], 9),
+                                              ([300, 20], [300, 77], 0), ([200, 60], [300, 77], 40)])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_attend_scales_not_finite(kvq, d, group, news, lens, window, which, value):
+    """A cached row whose scale is not finite makes NaN of the tokens that attend it
+    and leaves the others what they are."""
+    cache = make_pool(kvq, d, 30, 2, 16, d, group, 0)
+    table = make_batch(cache, 6, lens)
+    # one row of each sequence (of one group of values in one KV head): the last but
+    # one new token's, so that some tokens come before it and some after
+    at = [m - (2 if n < 10 else n // 2) for n, m in zip(news, lens)]
+    if news == [1, 1]:
+        at = [100, 400]  # attended by the first; past the end of the second
+    for s, t in enumerate(at):
+        if t < lens[s]:
+            scales = cache.k_scales if which == "k" else cache.v_scales
+            scales[int(table[s, t // 16]), 0, t % 16, d // group - 1] = value
+    q = rows(gen(4), sum(news), 4, d, torch.bfloat16) * 0.25
+    cu = np.concatenate([[0], np.cumsum(news)]).tolist()
+    with np.errstate(invalid="ignore"):
+        got = run_attend(kvq, cache, q, cu, lens, table, window=window)
+    for s, t in enumerate(at):
+        p = np.arange(lens[s] - news[s], lens[s])
+        bad = (p >= t) & ((p - t < window) if window else True) & (t < lens[s])
+        mine = got[cu[s]:cu[s + 1]]
+        assert mine[torch.from_numpy(bad), :2].isnan().all() and not mine[:, 2:].isnan().any()
+        assert not mine[torch.from_numpy(~bad)].isnan().any()
