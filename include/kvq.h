@@ -374,7 +374,7 @@ KVQ_API kvq_status kvq_qk_norm_rope(const void *q, const void *k, kvq_dtype dtyp
  *   k_hat, v_hat  [n_tokens][n_kv_heads][d] of dtype, contiguous, 16-byte
  *              aligned (written), or NULL: the values the new rows stand for,
  *              i.e. the inverse step of the fresh codes.  Rows of skipped
- *              tokens are left as they were.
+ *              tokens are left as they were.  They must not overlap k or v.
  *   n_tokens 0..2^31-1 (0: no-op); other arguments as above.
  */
 KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtype,
@@ -396,9 +396,9 @@ KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtyp
  * h of that token and KV head h / n_q:
  *   s_t = sm_scale <q, K_t>,  out = sum_t softmax(s)_t V_t, rounded to dtype.
  * A token that attends no row gets zeros; one whose query holds a NaN or an
- * infinity, or that attends a row with such a scale, gets NaN.  Rows of out that belong to no
- * sequence are left as they were.  Products run on the tensor cores with fp32
- * (or exact integer) sums.  Up to 16 query rows of a sequence and KV head
+ * infinity, or that attends a row with such a scale, gets NaN.  Rows of out that
+ * belong to no sequence are left as they were.  Products run on the tensor cores
+ * with fp32 (or exact integer) sums.  Up to 16 query rows of a sequence and KV head
  * (max_q_len * n_q): rotated queries in 15-bit fixed point, off by at most 1/32512
  * of the row's largest value; weights times V scales in 32-bit, off by 2^-28 of the
  * largest.  More: rotated queries, weights times V scales and, with g < d, the

@@ -2,6 +2,10 @@
 tables, rows that a mask hides, weights far below the largest, queries that are
 not finite, padding.  Helpers and tolerances: test_paged.py."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -13,6 +17,7 @@ from test_paged import (BOTH, attend_tolerance, check_large, check_rounded, gen,
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:invalid value:RuntimeWarning")]
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SHAPES = [(64, 64), (64, 32), (128, 128), (128, 32), (256, 256), (256, 64)]
 
 
@@ -213,6 +218,58 @@ def test_cache_fields_are_fixed(kvq):
     assert cache.k_packed.data_ptr() == cache.c.k_packed
 
 
+FIRST = r'''
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+from rotated_int4_kv_kvq_b200 import kvq, workloads as W
+dev = torch.device("cuda", 0)
+gen = torch.Generator(device=dev).manual_seed(5)
+for d, g in ((64, 64), (128, 32), (256, 256)):
+    signs = torch.from_numpy(W.make_signs(d)).to(dev)
+    table = kvq.rope_table(9000, d)
+    for new, heads in ((1, 1), (40, 2), (8000, 2)):
+        pages = -(-new // 64)
+        pt = torch.arange(pages, device=dev, dtype=torch.int32)[None]
+        cu = torch.tensor([0, new], device=dev, dtype=torch.int32)
+        ln = cu[1:].clone()
+        x = torch.randn((new, 6 * heads, d), generator=gen, device=dev).half()
+        q, k, v = x.split([4 * heads, heads, heads], 1)
+        pos, slots = kvq.paged_rows(cu, ln, pt, 64, new)
+        caches = []
+        for _ in range(2):
+            caches.append(kvq.PagedCache.empty(pages, heads, 64, d, g, signs))
+            for t in caches[-1].tensors()[:4]:
+                t.zero_()
+        def layer(cache):
+            kvq.kvq_paged_append(k, v, slots, cache, positions=pos, cos_sin=table)
+            qr, _ = kvq.kvq_qk_norm_rope(q, positions=pos, cos_sin=table)
+            return kvq.kvq_paged_attend(qr, cache, cu, ln, pt, max_q_len=new)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                o = layer(caches[0])
+        torch.cuda.current_stream().wait_stream(side)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, layer(caches[1])), (d, g, new)
+        for a, b in zip(caches[0].tensors(), caches[1].tensors()):
+            assert torch.equal(a, b)
+        del graph
+assert kvq.kvq_device_status() == 0
+print("ok")
+'''
+
+
+def test_first_calls_inside_graph_capture():
+    """Whatever a call looks up once per process can be looked up during a capture."""
+    r = subprocess.run([sys.executable, "-c", FIRST, ROOT], capture_output=True, text=True,
+                       timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
+    assert r.stdout.strip().endswith("ok")
 def test_key_output_without_keys(kvq):
     """What would come back unwritten is refused."""
     q, w = rows(gen(1), 3, 2, 64, torch.float16), torch.ones(64, device="cuda")
