@@ -400,7 +400,7 @@ KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtyp
  * belong to no sequence are left as they were.  Products run on the tensor cores
  * with fp32 (or exact integer) sums.  Up to 16 query rows of a sequence and KV head
  * (max_q_len * n_q): rotated queries in 15-bit fixed point, off by at most 1/32512
- * of the row's largest value; weights times V scales in 32-bit, off by 2^-28 of the
+ * of the row's largest value; weights times V scales in 32-bit, off by 2^-27 of the
  * largest.  More: rotated queries, weights times V scales and, with g < d, the
  * ratios of a row's K or V scales and their products with the codes rounded to
  * fp16 (2^-11 of a value each).  A score is then off by at most 3.1 2^-11

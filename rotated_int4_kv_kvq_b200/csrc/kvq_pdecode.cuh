@@ -17,7 +17,7 @@
 //            (error 1/32512 of its largest coordinate)
 //   values   O[i][n] = sum_t 16 c_V[t][i] P[t][n]     kind::i8, s32
 //            P: weight times V scale in 32-bit fixed point, four 8-bit
-//            slices (error 2^-28 of the largest so far)
+//            slices (error 2^-27 of the largest so far)
 // With several scales a row (g < d) the scores of each group accumulate in
 // columns of their own and each group of coordinates takes the P that carries
 // its scale; O keeps only those blocks.
@@ -25,12 +25,13 @@
 // Online softmax: the reference of a query moves only when a score exceeds it
 // by 7 in log2, the fixed point of P when a weight would overflow; either is
 // found by the vote in the barrier that P needs anyway.  Weights below half a step
-// of P are lost, of a tail of n faint tokens at most n 2^-28 of the largest; hence
-// four slices (three, with 7 bits of room: n 2^-17), and what P is made for only 4
-// bits below its top.  (The two batches below take 269 / 197 us with 2 bits of room
-// and 263 / 185 with 8, as tiles' maxima differ; with a vote that follows the tail
-// down instead 317 / 210.)  O is read back and accumulated in fp32 after every tile,
-// so it is never rescaled in place.
+// of P are lost, of a tail of n faint tokens at most n 2^-27 of the largest; hence
+// four slices (three, with 7 bits of room: n 2^-17), and what P is made for only 5
+// bits below its top.  (With less room more tiles are done twice.  32 sequences of
+// 4096 rows, 8 heads, 16 query rows each, d = 128, g = 32: 393 us with 4 bits, 371
+// with 5, 357 with 6, 349 with 8; a vote that follows the tail down instead: 209 us
+// where the batch of 64 below takes 180.)  O is read back and accumulated in fp32
+// after every tile, so it is never rescaled in place.
 //
 // A tile is 128 smem rows of 128 bytes (two tokens a row at d = 64, half a
 // token at d = 256).  A block is a pipeline of roles: four warps expand codes
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
     // ---------------- softmax: a token's scores -> weights ----------------
     const int row = tid;  // smem row; tokens row (and row + 128 at d = 64) of the tile
     constexpr int TPR = C::TPR;
-    // The fixed point of P counts in 2^-24 / cw; what it is made for lies in [8, 16) / cw.
+    // The fixed point of P counts in 2^-24 / cw; what it is made for lies in [4, 8) / cw.
     constexpr float kMost = 255.0f;
     float m[R], l[R], cw[R];
     float ks[TPR][NG], vs[TPR][NG];
@@ -676,10 +677,10 @@ __global__ void __launch_bounds__(kPdThreads, Pd<D, R, NG>::BLOCKS)
             float x = 0.0f;
 #pragma unroll
             for (int w = 0; w < 4; ++w) x = fmaxf(x, sh.red2[w][r]);
-            // the power of two that brings the largest into [8, 16); rows that need no
+            // the power of two that brings the largest into [4, 8); rows that need no
             // other keep theirs
             if ((moved >> r & 1u) || x * cw[r] > kMost) {
-              const int ex = min(max(257 - int(__float_as_uint(x) >> 23), 1), 225);
+              const int ex = min(max(256 - int(__float_as_uint(x) >> 23), 1), 225);
               cw[r] = __uint_as_float(uint32_t(ex) << 23);
               if (row == 0) sh.icwcur[r] = __uint_as_float(uint32_t(254 - ex) << 23);
             }
