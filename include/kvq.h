@@ -402,10 +402,12 @@ KVQ_API kvq_status kvq_paged_append(const void *k, const void *v, kvq_dtype dtyp
  * (max_q_len * n_q): rotated queries in 15-bit fixed point, off by at most 1/32512
  * of the row's largest value; weights times V scales in 32-bit, off by 2^-27 of the
  * largest.  More: rotated queries, weights times V scales and, with g < d, the
- * ratios of a row's K or V scales and their products with the codes rounded to
- * fp16 (2^-11 of a value each).  A score is then off by at most 3.1 2^-11
- * sm_scale |q| |K_t| (1.1 2^-11 with g = d), a weight times its V scale by 2^-11
- * of itself or 2^-31 of the largest V scale that the token attends.
+ * ratios of a row's K or V scales (and their products with the codes) are fp16
+ * operands.  With dtype KVQ_F16 each of them is two: a score is off by at most 2^-15
+ * sm_scale |q| |K_t|, a weight times its V scale by 2^-15 of itself.  With KVQ_BF16,
+ * whose results are rounded to 2^-8 anyway, each is one: 3.1 2^-11 sm_scale |q| |K_t|
+ * (1.1 2^-11 with g = d) and 3 2^-11.  Either way a weight times its V scale is off by
+ * up to 2^-31 of the largest V scale that the token attends.
  *
  *   q          [n_tokens][n_kv_heads * n_q][d], token stride q_stride (read)
  *   out        same, token stride out_stride (written); must not overlap q

@@ -154,10 +154,10 @@ cudaError_t few_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t strea
   return launch_join<D, R, 4, 4>(a, grid, stream);
 }
 
-template <int D, int NG>
-cudaError_t many_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t stream, unsigned* st) {
-  using C = Pc<D, NG>;
-  constexpr auto kern = kvq_paged_chunk_kernel<D, NG>;
+template <int D, int NG, bool TWO>
+cudaError_t many_rows_one(const PagedAttnArgs& args, int sm_count, cudaStream_t stream, unsigned* st) {
+  using C = Pc<D, NG, TWO>;
+  constexpr auto kern = kvq_paged_chunk_kernel<D, NG, TWO>;
   cudaError_t e = paged_setup<kern>(C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t items = (args.n_tokens * args.n_q + C::M - 1) / C::M + args.n_seqs;
@@ -171,6 +171,12 @@ cudaError_t many_rows(const PagedAttnArgs& args, int sm_count, cudaStream_t stre
   e = launch_paged(kern, grid, C::THREADS, C::SMEM, stream, a, st);
   if (e != cudaSuccess) return e;
   return launch_join<D, C::M, 8, 1>(a, grid, stream);
+}
+
+template <int D, int NG>
+cudaError_t many_rows(const PagedAttnArgs& a, int sm_count, cudaStream_t stream, unsigned* st) {
+  return a.dtype == kDtF16 ? many_rows_one<D, NG, true>(a, sm_count, stream, st)
+                           : many_rows_one<D, NG, false>(a, sm_count, stream, st);
 }
 
 template <int D>

@@ -24,11 +24,19 @@
 // and the codes are multiplied by the ratios s_j / s_max: ratio and product are
 // rounded to fp16, 2^-11 each, so a score is off by three times that at most.
 //
+// That is less than a bf16 result is rounded by, but not less than an fp16 one: with
+// scores of a few units fp16 results were 2 to 4 times as far off as their rounding.
+// For fp16 activations (TWO) each rounded operand is therefore two: Q and what the
+// rounding leaves of it (in tensor memory), P likewise (a slot of S holds both), and
+// the ratio's first 8 bits, whose products with codes are exact, and its rest; the
+// products of two rests are left out.  2 (g < d: 3) MMAs for one, and tiles of 64
+// tokens so that all of it fits.
+//
 // A block holds 256 query rows (two tiles of 128; one at d = 256, where tensor
 // memory holds one): while the tensor cores work for one tile the other one's
 // scores become weights.  Roles: four warps of softmax a tile (a thread a row;
 // they also rotate their rows in and out), four that turn packed codes into
-// fp16 operands (a thread a token), one that issues MMAs, one that looks pages
+// fp16 operands (a thread or two a token), one that issues MMAs, one that looks pages
 // up.  P overwrites S in tensor memory and is read from there.
 //
 // Measured: 4096 new tokens over 16,384 rows, 8 KV heads of 4 queries, d = 128:
@@ -43,17 +51,23 @@
 
 namespace kvq {
 
-template <int D_, int NG_>
+template <int D_, int NG_, bool TWO_>
 struct Pc {
   static constexpr int D = D_, NG = NG_, G = D / NG;
+  static constexpr bool TWO = TWO_;             // operands in two halves
+  static constexpr bool TWO_KV = TWO && NG > 1; // (codes alone are exact)
   static constexpr int NT = D == 256 ? 1 : 2;   // row tiles of a block
   static constexpr int M = 128 * NT;            // query rows of an item
-  static constexpr int KT = 128;                // tokens of a tile
-  static constexpr int KS = D == 256 ? 1 : 2;   // K and V operands in shared memory
+  static constexpr int KT = TWO ? 64 : 128;     // tokens of a tile
+  // K and V operands in shared memory
+  static constexpr int KS = D == 256 && (!TWO || TWO_KV) ? 1 : 2;
   static constexpr int NCH = D / 64;            // 128-byte columns of a row
-  static constexpr int TILE = NCH * 16384;      // Q tile, K or V: 128 rows
-  static constexpr int oQ = 0, oK = NT * TILE, oV = oK + KS * TILE;
-  static constexpr int SMEM = oV + KS * TILE + 1024;
+  static constexpr int QCOL = 128 * 128, KCOL = KT * 128;  // bytes of one: of Q, of K or V
+  static constexpr int TILE = NCH * QCOL;       // Q tile
+  static constexpr int KVH = NCH * KCOL;        // K or V, a half
+  static constexpr int KV = TWO_KV ? 2 * KVH : KVH;
+  static constexpr int oQ = 0, oK = NT * TILE, oV = oK + KS * KV;
+  static constexpr int SMEM = oV + KS * KV + 1024;
   static constexpr int WARPS = NT * 4 + 8;      // whole warpgroups, two warps idle
   static constexpr int THREADS = WARPS * 32;
   // Registers a thread: the softmax threads hold a whole row when they rotate it.
@@ -62,7 +76,9 @@ struct Pc {
   static constexpr bool SPLIT = NT == 2;
   static constexpr int REGS_MORE = 176, REGS_LESS = 80;
   static constexpr int W_DEQ = NT * 4, W_MMA = W_DEQ + 4, W_PAGE = W_MMA + 1;
-  static constexpr uint32_t colO = 256;         // tensor memory: S/P slots, then O
+  // Tensor memory: S/P slots, the second halves of Q, then O.
+  static constexpr uint32_t colQ = 128, colO = 256;
+  static_assert(2 * KT + (TWO ? NT * D / 2 : 0) <= 256, "tensor memory");
   static_assert(SMEM + 4096 <= 232448, "shared memory");
 };
 
@@ -153,6 +169,17 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A pair of values as fp16, and what that leaves of them.
+template <bool TWO>
+__device__ __forceinline__ uint32_t pc_half(float x, float y, uint32_t& rest) {
+  const uint32_t h = float2_to_half2_bits(x, y);
+  if constexpr (TWO) {
+    const float2 f = half2_bits_to_float2(h);
+    rest = float2_to_half2_bits(x - f.x, y - f.y);
+  }
+  return h;
+}
+
 // Factor for a row whose largest rotated value is `top`: a power of two that
 // brings it into [2^8, 2^9), far from fp16's smallest and largest, with the sign
 // of the softmax scale; `back` undoes it and applies the scale.  A row with an
@@ -166,11 +193,13 @@ __device__ __forceinline__ float pc_scale(float top, float qscale, float& back) 
 }
 
 // d <= 128: a thread rotates its own row, in registers (the two-lane real FFT
-// codelets, or a Walsh-Hadamard network), into the Q tile.  Returns the factor
-// from the row's products to log2 scores.
-template <int D, int ROT>
+// codelets, or a Walsh-Hadamard network), into the Q tile, a second half into the
+// columns `rest` of tensor memory (then by whole warps).  Returns the factor from
+// the row's products to log2 scores.
+template <int D, int ROT, bool TWO>
 __device__ __forceinline__ float pc_query_row(const PagedAttnArgs& a, const uint16_t* src,
-                                              uint32_t tile, int r, const uint32_t* sign) {
+                                              uint32_t tile, int r, const uint32_t* sign,
+                                              uint32_t rest) {
   using C = Cfg<D, ROT, 1>;
   f2 u[C::NW], Y[C::P];
 #pragma unroll
@@ -188,14 +217,19 @@ __device__ __forceinline__ float pc_query_row(const PagedAttnArgs& a, const uint
   const float top = absmax2<C::P>(Y);
   float back;
   const float sg = pc_scale(top, a.qscale, back);
+  uint32_t low[16];
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {  // columns 0 4 1 5 2 6 3 7 of each eight
     const f2 p = Y[4 * i], q = Y[4 * i + 1], s = Y[4 * i + 2], t = Y[4 * i + 3];
+    uint32_t* l = low + 4 * (i & 3);
     sts128(tile + uint32_t(i >> 3) * 16384 + uint32_t(r) * 128 + (uint32_t((i ^ r) & 7) << 4),
-           float2_to_half2_bits(lo2(p) * sg, lo2(s) * sg),
-           float2_to_half2_bits(hi2(p) * sg, hi2(s) * sg),
-           float2_to_half2_bits(lo2(q) * sg, lo2(t) * sg),
-           float2_to_half2_bits(hi2(q) * sg, hi2(t) * sg));
+           pc_half<TWO>(lo2(p) * sg, lo2(s) * sg, l[0]),
+           pc_half<TWO>(hi2(p) * sg, hi2(s) * sg, l[1]),
+           pc_half<TWO>(lo2(q) * sg, lo2(t) * sg, l[2]),
+           pc_half<TWO>(hi2(q) * sg, hi2(t) * sg, l[3]));
+    if constexpr (TWO) {
+      if ((i & 3) == 3) tmem_st16(rest + uint32_t(i & ~3) * 4, low);
+    }
   }
   return back * C::KAPPA_INV;  // both ways the same
 }
@@ -252,11 +286,14 @@ __device__ __forceinline__ void pc_result_row(const PagedAttnArgs& a, f2 (&Y)[D 
 }
 
 // d = 256: a lane pair rotates a row (every lane of the warp takes part; rows
-// that are not `there` read nothing).  The factor comes back in both lanes.
-template <int ROT>
+// that are not `there` read nothing).  The factor comes back in both lanes.  The
+// second halves reach their rows' lanes of tensor memory through the rows' places
+// in the Q tile; r0 is the warp's first row, `half` which 16 of its rows these are.
+template <int ROT, bool TWO>
 __device__ __forceinline__ float pc_query_pair(const PagedAttnArgs& a, const uint16_t* src,
-                                               bool there, uint32_t tile, int r, int t,
-                                               const uint32_t* sign) {
+                                               bool there, uint32_t tile, int r0, int half,
+                                               const uint32_t* sign, uint32_t rest) {
+  const int lane = threadIdx.x & 31, t = lane & 1, r = r0 + 16 * half + lane / 2;
   using C = Cfg<256, ROT, 2>;
   f2 u[C::NW], Y[C::P];
   const uint32_t* sg = sign + t * C::NW;
@@ -287,27 +324,58 @@ __device__ __forceinline__ float pc_query_pair(const PagedAttnArgs& a, const uin
   top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
   float back;
   const float mul = pc_scale(top, a.qscale, back);
+  auto store = [&](auto low) {  // the halves, or what they leave, into the Q tile
+    constexpr bool LOW = decltype(low)::value;
+    auto word = [](float x, float y) {
+      uint32_t rest = 0;
+      const uint32_t h = pc_half<LOW>(x, y, rest);
+      return LOW ? rest : h;
+    };
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {  // a quarter of the row: one 128-byte column
-    // (thread 1's second half of the Walsh-Hadamard pair is negated)
-    const float m = ROT == kRotSRHT && t == 1 && h == 1 ? -mul : mul;
-    const uint32_t at = tile + uint32_t(global_y<C>(t, 64 * h) >> 6) * 16384 + uint32_t(r) * 128;
+    for (int h = 0; h < 2; ++h) {  // a quarter of the row: one 128-byte column
+      // (thread 1's second half of the Walsh-Hadamard pair is negated)
+      const float m = ROT == kRotSRHT && t == 1 && h == 1 ? -mul : mul;
+      const uint32_t at = tile + uint32_t(global_y<C>(t, 64 * h) >> 6) * 16384 + uint32_t(r) * 128;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const f2* y = Y + 32 * h + 4 * i;
-      sts128(at + (uint32_t((i ^ r) & 7) << 4), float2_to_half2_bits(lo2(y[0]) * m, lo2(y[2]) * m),
-             float2_to_half2_bits(hi2(y[0]) * m, hi2(y[2]) * m),
-             float2_to_half2_bits(lo2(y[1]) * m, lo2(y[3]) * m),
-             float2_to_half2_bits(hi2(y[1]) * m, hi2(y[3]) * m));
+      for (int i = 0; i < 8; ++i) {
+        const f2* y = Y + 32 * h + 4 * i;
+        sts128(at + (uint32_t((i ^ r) & 7) << 4), word(lo2(y[0]) * m, lo2(y[2]) * m),
+               word(hi2(y[0]) * m, hi2(y[2]) * m), word(lo2(y[1]) * m, lo2(y[3]) * m),
+               word(hi2(y[1]) * m, hi2(y[3]) * m));
+      }
     }
+  };
+  if constexpr (TWO) {
+    store(std::true_type{});
+    __syncwarp();
+    const int mine = r0 + lane;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      uint32_t v[16];
+      tmem_ld<16>(rest + 16 * c, v);  // (the other 16 rows')
+      tmem_wait_ld();
+      if (lane >> 4 == half) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int piece = 4 * c + p;
+          const uint4 x = lds128(tile + uint32_t(piece >> 3) * 16384 + uint32_t(mine) * 128 +
+                                 (uint32_t((piece ^ mine) & 7) << 4));
+          v[4 * p] = x.x, v[4 * p + 1] = x.y, v[4 * p + 2] = x.z, v[4 * p + 3] = x.w;
+        }
+      }
+      tmem_st16(rest + 16 * c, v);
+    }
+    tmem_wait_st();  // (the other half reads what is stored here)
+    __syncwarp();
   }
+  store(std::false_type{});
   return back * C::KAPPA_INV;  // both ways the same
 }
 
-template <int D, int NG>
-__global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
+template <int D, int NG, bool TWO>
+__global__ void __launch_bounds__(Pc<D, NG, TWO>::THREADS, 1)
     kvq_paged_chunk_kernel(const PagedAttnArgs a, unsigned* status) {
-  using C = Pc<D, NG>;
+  using C = Pc<D, NG, TWO>;
   constexpr int NT = C::NT, M = C::M, KT = C::KT, KS = C::KS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PcShared sh;
@@ -421,12 +489,18 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         const int slot = NT == 2 ? x : i & 1;
         if (lane == 0) {
           tc_fence_after();
-          const uint32_t q = sbase + C::oQ + x * C::TILE, k = sbase + C::oK + (i % KS) * C::TILE;
+          const uint32_t q = sbase + C::oQ + x * C::TILE, k = sbase + C::oK + (i % KS) * C::KV;
+          const uint32_t d = tmem + slot * KT;
 #pragma unroll 1
-          for (int s = 0; s < D / 16; ++s)
-            mma_f16(tmem + slot * 128,
-                    smem_desc(q + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128),
-                    smem_desc(k + (s / 4) * 16384 + (s % 4) * 32, 16, 1024, kSw128), idS, s > 0);
+          for (int s = 0; s < D / 16; ++s) {
+            const uint64_t dq = smem_desc(q + (s / 4) * C::QCOL + (s % 4) * 32, 16, 1024, kSw128);
+            const uint32_t ks = k + (s / 4) * C::KCOL + (s % 4) * 32;
+            const uint64_t dk = smem_desc(ks, 16, 1024, kSw128);
+            mma_f16(d, dq, dk, idS, s > 0);
+            if constexpr (TWO) mma_f16_ts(d, tmem + C::colQ + x * (D / 2) + s * 8, dk, idS, true);
+            if constexpr (C::TWO_KV)
+              mma_f16(d, dq, smem_desc(ks + C::KVH, 16, 1024, kSw128), idS, true);
+          }
           mma_commit(bar(sh.sdone[slot]));
           if (x == NT - 1 || !two) mma_commit(bar(sh.kfree[i % KS]));
         }
@@ -436,11 +510,18 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         const int slot = NT == 2 ? x : i & 1;
         if (lane == 0) {
           tc_fence_after();
-          const uint32_t v = sbase + C::oV + (i % KS) * C::TILE;
+          const uint32_t v = sbase + C::oV + (i % KS) * C::KV;
+          const uint32_t d = tmem + C::colO + x * 128;
 #pragma unroll 1
-          for (int s = 0; s < KT / 16; ++s)
-            mma_f16_ts(tmem + C::colO + x * 128, tmem + slot * 128 + s * 8,
-                       smem_desc(v + s * 2048, 16384, 1024, kSw128), idO, !first || s > 0);
+          for (int s = 0; s < KT / 16; ++s) {
+            // (in two halves: 16 columns of each, in turn)
+            const uint32_t p = tmem + slot * KT + (TWO ? s / 2 * 32 + s % 2 * 8 : s * 8);
+            const uint64_t dv = smem_desc(v + s * 2048, C::KCOL, 1024, kSw128);
+            mma_f16_ts(d, p, dv, idO, !first || s > 0);
+            if constexpr (TWO) mma_f16_ts(d, p + 16, dv, idO, true);
+            if constexpr (C::TWO_KV)
+              mma_f16_ts(d, p, smem_desc(v + C::KVH + s * 2048, C::KCOL, 1024, kSw128), idO, true);
+          }
           mma_commit(bar(sh.odone[slot]));
           if (x == NT - 1 || !two) mma_commit(bar(sh.vfree[i % KS]));
         }
@@ -494,16 +575,18 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         }
       }
     } else if (warp < C::W_MMA) {
-      // ---------------- packed codes -> fp16 operands, a thread a token ----------------
-      const int t = tid - C::W_DEQ * 32;
-      constexpr int NP = D / 32;  // 16-byte pieces of a row
+      // ---------------- packed codes -> fp16 operands ----------------
+      // A thread takes a token, or half of one (and then half of its groups).
+      constexpr int TPT = 128 / KT, NP = D / 32 / TPT;  // 16-byte pieces of a thread
+      constexpr int NGT = NG > 1 ? NG / TPT : 1;
+      const int t = (tid - C::W_DEQ * 32) % KT, part = (tid - C::W_DEQ * 32) / KT;
       uint4 kreg[NP], vreg[NP];
       float ksc[NG], vsc[NG];
       auto load = [&](int i) {
         const PcTile& e = sh.tiles[i % kPcRing];
         const int64_t r = e.row[t >> 4] + (t & 15);
-        const uint4* kp = reinterpret_cast<const uint4*>(a.k_packed + r * (D / 2));
-        const uint4* vp = reinterpret_cast<const uint4*>(a.v_packed + r * (D / 2));
+        const uint4* kp = reinterpret_cast<const uint4*>(a.k_packed + r * (D / 2)) + part * NP;
+        const uint4* vp = reinterpret_cast<const uint4*>(a.v_packed + r * (D / 2)) + part * NP;
         const bool there =
             (e.have >> (t >> 4) & 1u) && e.t0 + t >= e.lo && e.t0 + t < e.hi;
 #pragma unroll
@@ -515,24 +598,32 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         }
       };
       auto convert = [&](const uint4 (&w)[NP], const float (&sc)[NG], float top, uint32_t tile) {
-        const float inv = top > 0.0f ? 1.0f / top : 0.0f;
+        const float inv = top >= 0x1p-126f ? 1.0f / top : 0.0f;
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-          uint32_t f = 0;
+          uint32_t f = 0, fl = 0;
           if constexpr (NG > 1) {
-            const float x = top > 0.0f ? sc[k * 32 / C::G] * inv : 0.0f;
-            f = float2_to_half2_bits(x, x);
+            const int g = k * 32 / C::G;
+            const float own = TPT == 2 && part != 0 ? sc[NG - NGT + g] : sc[g];
+            const float x = inv > 0.0f ? own * inv : 0.0f;
+            // In two halves: 8 bits, so that products with codes are exact, and the rest.
+            const float h = TWO ? __uint_as_float(__float_as_uint(x) & 0xFFFF0000u) : x;
+            f = float2_to_half2_bits(h, h);
+            fl = float2_to_half2_bits(x - h, x - h);
           }
           const uint32_t words[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+          const int kk = part * NP + k;  // piece of the row
+          const uint32_t to = tile + uint32_t(kk / 2) * C::KCOL + uint32_t(t) * 128;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint4 h = codes_to_half(words[j]);
+            const uint4 h = codes_to_half(words[j]);
+            const uint32_t at = to + (uint32_t(((kk & 1) * 4 + j) ^ (t & 7)) << 4);
             if constexpr (NG > 1)
-              h = make_uint4(hmul2(h.x, f), hmul2(h.y, f), hmul2(h.z, f), hmul2(h.w, f));
-            const int c = (k & 1) * 4 + j;  // 16-byte column of the 128
-            sts128(tile + uint32_t(k / 2) * 16384 + uint32_t(t) * 128 +
-                       (uint32_t(c ^ (t & 7)) << 4),
-                   h.x, h.y, h.z, h.w);
+              sts128(at, hmul2(h.x, f), hmul2(h.y, f), hmul2(h.z, f), hmul2(h.w, f));
+            else
+              sts128(at, h.x, h.y, h.z, h.w);
+            if constexpr (C::TWO_KV)
+              sts128(at + C::KVH, hmul2(h.x, fl), hmul2(h.y, fl), hmul2(h.z, fl), hmul2(h.w, fl));
           }
         }
         fence_proxy_async_smem();
@@ -560,16 +651,18 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
         const int vexp = max(int(__float_as_uint(x) >> 23) - 133, -126);
         const float vmul = __uint_as_float(uint32_t(127 - vexp) << 23);
         // ring of four: the softmax of tile i - 4 is behind V's wait of tile i - 1
-        sh.ks[i & 3][t] = ktop;
-        sh.vs[i & 3][t] = vtop * vmul;
-        if (t == 0) sh.vexp[i & 3] = vexp;
+        if (part == 0) {
+          sh.ks[i & 3][t] = ktop;
+          sh.vs[i & 3][t] = vtop * vmul;
+          if (t == 0) sh.vexp[i & 3] = vexp;
+        }
         arrive(sh.scfull[i & 3]);
         // K, then V through the same code (for the instruction cache)
         float top = ktop;
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           if (i >= KS) wait(kv ? sh.vfree[i % KS] : sh.kfree[i % KS], i / KS - 1);
-          convert(kreg, ksc, top, sbase + (kv ? C::oV : C::oK) + (i % KS) * C::TILE);
+          convert(kreg, ksc, top, sbase + (kv ? C::oV : C::oK) + (i % KS) * C::KV);
           arrive(kv ? sh.vfull[i % KS] : sh.kfull[i % KS]);
 #pragma unroll
           for (int k = 0; k < NP; ++k) kreg[k] = vreg[k];
@@ -611,15 +704,19 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
             return a.q + (int64_t(e.c0) + tok) * a.q_stride +
                    (int64_t(e.head) * a.n_q + (g - tok * a.n_q)) * D;
           };
+          const uint32_t rest = tlane + C::colQ + x * (D / 2);
           if constexpr (D <= 128) {
-            if (lane < nr)
-              rowc = pc_query_row<D, ROT>(a, source(lane), qtile, w4 * 32 + lane, sh.sign_in);
+            if (TWO ? nr > 0 : lane < nr) {  // (the whole warp stores to tensor memory)
+              const float f = pc_query_row<D, ROT, TWO>(a, source(min(lane, nr - 1)), qtile,
+                                                        w4 * 32 + lane, sh.sign_in, rest);
+              if (lane < nr) rowc = f;
+            }
           } else {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {  // rows 0..15, then 16..31
               const int r = 16 * h + lane / 2;
-              const float f = pc_query_pair<ROT>(a, source(min(r, max(nr - 1, 0))), r < nr, qtile,
-                                                 w4 * 32 + r, lane & 1, sh.sign_in);
+              const float f = pc_query_pair<ROT, TWO>(a, source(min(r, max(nr - 1, 0))), r < nr,
+                                                      qtile, w4 * 32, h, sh.sign_in, rest);
               const float g = __shfl_sync(kFull, f, 2 * (lane & 15));
               if (lane >> 4 == h && lane < nr) rowc = g;
             }
@@ -629,6 +726,10 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
           queries(std::integral_constant<int, kRotSRFT>{});
         else
           queries(std::integral_constant<int, kRotSRHT>{});
+        if constexpr (TWO) {
+          tmem_wait_st();
+          tc_fence_before();
+        }
         fence_proxy_async_smem();
         if (active) arrive(sh.qfull[x]);
         pos = e.p0 + (e.row0 + x * 128 + min(w4 * 32 + lane, max(rows - 1, 0))) / a.n_q;
@@ -638,14 +739,14 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
       }
       if (active) {
         const int slot = NT == 2 ? x : i & 1;
-        const uint32_t tS = tlane + slot * 128;
+        const uint32_t tS = tlane + slot * KT;
         wait(sh.sdone[slot], NT == 2 ? used : i >> 1);
         wait(sh.scfull[i & 3], i >> 2);
         tc_fence_after();
         // first and last position of the warp's rows decide on masks
         const int pf = __shfl_sync(kFull, pos, 0), pl = __shfl_sync(kFull, pos, 31);
         const bool whole = e.t0 + KT - 1 <= pf && (a.window == 0 || e.t0 > pl - a.window) &&
-                           e.have == 0xFFu;
+                           e.have == (1u << (KT / 16)) - 1;
         const int hi = pos - e.t0;                                     // last column seen
         const int lo = a.window > 0 ? pos - a.window + 1 - e.t0 : 0;   // first
         auto seen = [&](int c) {  // bit j: column c + j of 32 is seen
@@ -737,7 +838,7 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
           f2 l2 = mk2(0.0f, 0.0f);
 #pragma unroll 1
           for (int c = 0; c < KT; c += 32) {
-            uint32_t s[32], p[16];
+            uint32_t s[32], p[TWO ? 32 : 16];
             tmem_ld<32>(tS + c, s);
             const uint32_t sm = MASK ? seen(c) : 0u;
             tmem_wait_ld();
@@ -760,10 +861,13 @@ __global__ void __launch_bounds__(Pc<D, NG>::THREADS, 1)
                 const f2 pp = mk2(ex2(z0), ex2(z1));
                 l2 = add2(l2, pp);
                 const f2 wv = mul2(pp, vv);
-                p[(j + b) / 2] = float2_to_half2_bits(lo2(wv), hi2(wv));
+                p[(j + b) / 2] = pc_half<TWO>(lo2(wv), hi2(wv), p[(TWO ? 16 : 0) + (j + b) / 2]);
               }
             }
-            tmem_st16(tS + c / 2, p);  // over columns of S that have been read
+            if constexpr (TWO)  // over columns of S that have been read
+              tmem_st32(tS + c, p);
+            else
+              tmem_st16(tS + c / 2, p);
           }
           l = fmaf(lo2(l2) + hi2(l2), __uint_as_float(uint32_t(127 - dv) << 23), l);
         };

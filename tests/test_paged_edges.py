@@ -12,8 +12,9 @@ import torch
 
 import oracle.kvq_oracle as O
 from rotated_int4_kv_kvq_b200 import workloads as W
-from test_paged import (BOTH, attend_tolerance, check_large, check_rounded, gen, kvq,
-                         make_batch, make_pool, np64, poison, rows, run_attend)  # noqa: F401
+from test_paged import (BOTH, attend_f64, attend_tolerance, check_large, check_rounded,
+                         gen, kvq, make_batch, make_pool, np64, poison, rows,
+                         run_attend)  # noqa: F401
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:invalid value:RuntimeWarning")]
 
@@ -306,3 +307,27 @@ def test_attend_scales_not_finite(kvq, d, group, news, lens, window, which, valu
         mine = got[cu[s]:cu[s + 1]]
         assert mine[torch.from_numpy(bad), :2].isnan().all() and not mine[:, 2:].isnan().any()
         assert not mine[torch.from_numpy(~bad)].isnan().any()
+
+
+@pytest.mark.parametrize("rot", [O.SRFT, O.SRHT])
+@pytest.mark.parametrize("d,group", [(64, 64), (64, 32), (128, 128), (128, 64), (128, 32), (256, 256),
+                                     (256, 128), (256, 64), (256, 32)])
+@pytest.mark.parametrize("nq,news,lens,window", [(4, [300, 5], [1000, 700], 0), (1, [520], [900], 100)])
+def test_attend_many_rows_fp16_keeps_its_bits(kvq, rot, d, group, nq, news, lens, window):
+    """What a chunk's fp16 results are off by is their own rounding: uniform within half
+    a step of at most 2^-10 |x|, so 2^-11 / sqrt(3) of the whole by the 2-norm, and 5%
+    for all before it.  (Each row besides within its bound in the header.)"""
+    cache = make_pool(kvq, d, sum(-(-m // 16) for m in lens), 4, 16, d, group, rot)
+    table = make_batch(cache, 6, lens)
+    cu = np.concatenate([[0], np.cumsum(news)]).tolist()
+    q = (2 * torch.randn((cu[-1], 4 * nq, d), generator=gen(5), device="cuda")).half()
+    dev = dict(device="cuda", dtype=torch.int32)
+    got = kvq.kvq_paged_attend(q, cache, torch.tensor(cu, **dev), torch.tensor(lens, **dev), table,
+                               max_q_len=max(news), window=window)
+    assert kvq.kvq_device_status() == 0
+    ref, mass, far = attend_f64(q, cache, cu, lens, table, window)
+    err = (got.double() - ref).norm(dim=-1)
+    tol = 2.0 ** -11 * ref.norm(dim=-1) + (torch.expm1(2 * 2.0 ** -15 * far) + 2.0 ** -15) * mass
+    assert (err <= tol).all(), (err / tol).max().item()
+    whole = (err.square().sum().sqrt() / ref.norm()).item()
+    assert whole <= 1.05 * 2.0 ** -11 / 3 ** 0.5, whole
