@@ -6,11 +6,12 @@
 // results but for rounding: one warp per vector (the layout of kvq_wide.cuh) for
 // few rows, where the length of one row's chain is the time, and one thread (d =
 // 256: two) per vector (kvq_codec.cuh) for many, where instructions are: the
-// warp-wide transform spends most of its own on shuffles.  With norm, rotation
-// and dequantized rows, d = 128: 8180 rows 8.5 us (a warp a row), 262,144 rows
-// 123 us (a thread a row; bytes alone would take 24.5.  4.7 thousand
-// instructions a warp and 32 rows, issued in 36% of the clocks: 168 registers
-// leave 12 warps an SM, too few to hide the chain of each).
+// warp-wide transform spends most of its own on shuffles.  With norm and rotation,
+// d = 128, with dequantized rows and without: 8180 rows 8.5 and 6.5 us (a warp a
+// row), 262,144 rows 121 and 98 us (a thread a row; bytes alone would take 24.5, the
+// codec's own forward and inverse of as many contiguous rows 18 and 19.  4.7
+// thousand instructions a warp and 32 rows, issued in 36% of the clocks: 168
+// registers leave 12 warps an SM, too few to hide the chain of each).
 #pragma once
 
 #include "kvq_codec.cuh"

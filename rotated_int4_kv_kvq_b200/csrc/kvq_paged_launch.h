@@ -77,10 +77,10 @@ constexpr int few_rows_item(int d, int group, int64_t rows) {
 constexpr int64_t kMaxBlocks = 148 * 4;  // of the few-rows kernel
 constexpr int64_t kMaxChunkBlocks = 148;  // of the many-rows kernel, one an SM
 // Up to this many rows of a sequence and KV head the few-rows kernel runs.
-// At 30 rows, many- against few-rows kernel: 32 sequences of 4096 rows and 8
-// heads 182 / 362 us (d = 64) to 402 / 575 (d = 256); one sequence and head 17.9
-// / 21.3 (d = 64), but 27.9 / 22.7 (d = 128) and 43.0 / 30.9 (d = 256).  The
-// limit favours large batches: lengths are known on the device only.
+// At 30 rows, many- against few-rows kernel, us: 32 sequences of 4096 rows and 8
+// heads, bf16 193 / 421 (d = 64) to 407 / 595 (d = 256), fp16 288 / 421 to 661 / 596;
+// one sequence and head, bf16 19.3 / 22.7 (d = 64) to 43.9 / 31.4 (d = 256), fp16 24.2
+// / 22.7 to 60.5 / 31.4.  The limit favours large batches.
 constexpr int64_t kFewRows = 16;
 constexpr int64_t attn_workspace(int d, int64_t rows) {
   const int64_t slots = rows <= kFewRows ? kMaxBlocks * 2 * 16

@@ -40,12 +40,12 @@
 // the MMAs, one looks the pages up.  Operands, scores and results are
 // double-buffered, so the roles work on neighbouring tiles at once.
 //
-// Measured: 512 KV heads of 16,384 rows, one query, d = 64, g = 64: 254 us, 2.4
-// TB/s, 36% of the copy rate; 64 ragged sequences up to 8192 rows, 8 heads of 4
-// queries, d = 128, g = 32: 176 us, 2.0 TB/s, 30%.  No unit is
-// full: the schedulers issue in 46% of the clocks (3.8 thousand instructions a
-// tile at d = 64), DRAM and the tensor cores are below a third.  Waits are 45%
-// long scoreboard, 17% instruction fetch: the roles' latency bounds it.
+// Measured: 512 KV heads of 16,384 rows, one query, d = 64, g = 64: 262 us, 2.3
+// TB/s, 35% of the copy rate; 64 ragged sequences up to 8192 rows, 8 heads of 4
+// queries, d = 128, g = 32: 184 us, 1.9 TB/s, 29%.  No unit is full: the schedulers
+// issue in 46% of the clocks (3.9 thousand instructions a tile at d = 64), DRAM and
+// the tensor cores are below a third.  Waits are 46% long scoreboard, 17%
+// instruction fetch: the roles' latency bounds it.
 #pragma once
 
 #include "kvq_sched.cuh"
