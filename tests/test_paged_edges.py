@@ -331,3 +331,22 @@ def test_attend_many_rows_fp16_keeps_its_bits(kvq, rot, d, group, nq, news, lens
     assert (err <= tol).all(), (err / tol).max().item()
     whole = (err.square().sum().sqrt() / ref.norm()).item()
     assert whole <= 1.05 * 2.0 ** -11 / 3 ** 0.5, whole
+
+
+def test_paged_rows_captured(kvq):
+    """Computed on the device alone: a captured call follows its inputs."""
+    def batch(cu, lens, table):
+        return [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (cu, lens, table)]
+    first = batch([0, 3, 4], [20, 40], [[5, 9, 1], [3, 4, 2]])
+    graph = torch.cuda.CUDAGraph()
+    kvq.paged_rows(*first, 16, 6)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        pos, slots = kvq.paged_rows(*first, 16, 6)
+    for other in (first, batch([1, 1, 6], [0, 50], [[5, 9, 1], [-1, 4, 2]])):
+        for a, b in zip(first, other):
+            a.copy_(b)
+        graph.replay()
+        want = kvq.paged_rows(*(x.cpu() for x in other), 16, 6)
+        assert pos.tolist() == want[0].tolist() and slots.tolist() == want[1].tolist()
+    del graph
